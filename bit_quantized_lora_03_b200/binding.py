@@ -8,6 +8,7 @@ calls raise.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -28,6 +29,7 @@ QLORA_STATIC_SCRATCH_BYTES = 8 << 20
 QLORA_DEV_NONFINITE = 1
 QLORA_DEV_TIMEOUT = 2
 QLORA_DEV_LAUNCH = 4
+QLORA_DEV_TARGET = 8
 
 # Every symbol the header declares, with its ctypes signature.
 _PTR = ctypes.c_void_p
@@ -75,8 +77,21 @@ SIGNATURES = {
     "qlora_bwd_dropout_workspace_bytes": (ctypes.c_size_t, [_I64, _I64, _I64, _I64]),
     "qlora_dropout_apply": (ctypes.c_int, [_PTR, _I64, _I64, ctypes.c_float, ctypes.c_uint64, _PTR,
                                            _PTR]),
+    "qlora_linear_fwd_epilogue": (ctypes.c_int, [_PTR, _I64, _PTR, _PTR, _PTR, _I64, ctypes.c_float,
+                                                 _PTR, ctypes.c_int, _PTR, _PTR, _PTR, _PTR, _PTR,
+                                                 ctypes.c_size_t, _PTR]),
+    "qlora_epilogue_bwd": (ctypes.c_int, [_PTR, _PTR, _I64, _I64, ctypes.c_int, _PTR, _PTR, _PTR,
+                                          ctypes.c_size_t, _PTR]),
+    "qlora_epilogue_bwd_workspace_bytes": (ctypes.c_size_t, [_I64, _I64]),
+    "qlora_norm_residual_fwd": (ctypes.c_int, [_PTR, _PTR, _I64, _I64, _PTR, _PTR, _I64,
+                                               ctypes.c_float, _PTR, ctypes.c_float, _PTR, _PTR,
+                                               _PTR, _PTR, _PTR]),
+    "qlora_norm_residual_bwd": (ctypes.c_int, [_PTR, _PTR, _PTR, _PTR, _I64, _I64, _PTR, _PTR, _I64,
+                                               ctypes.c_float, _PTR, _PTR, _PTR, _PTR, _PTR, _PTR,
+                                               _PTR, _PTR, _PTR, ctypes.c_size_t, _PTR]),
+    "qlora_norm_residual_bwd_workspace_bytes": (ctypes.c_size_t, [_I64, _I64]),
 }
-KERNEL_KINDS = 8
+KERNEL_KINDS = 12
 
 
 class NF4WeightDesc(ctypes.Structure):
@@ -383,6 +398,192 @@ def qlora_linear_bwd_dropout(dY: torch.Tensor, X: torch.Tensor, p: PackedNF4, L1
                                         ws.data_ptr(), ws.numel(), _stream(stream))
     _check(rc, "qlora_linear_bwd_dropout")
     return dX, dL1, dL2
+
+
+# ------------------------------------------------------------------------------------------
+# The operators around the linear. They run on the device of their tensors (all on one) and on the
+# current stream there, or on `stream`; what they allocate (outputs, workspace) is allocated on
+# that stream, one workspace per call, so that calls on two streams, and graphs captured from them,
+# share none.
+# ------------------------------------------------------------------------------------------
+_NO_GUARD = contextlib.nullcontext()
+
+
+def _guard(t: torch.Tensor, stream):
+    """Makes the device of `t`, and `stream` if given, current for the call."""
+    if not t.is_cuda:
+        raise ValueError(f"expected CUDA tensors, got one on {t.device}")
+    if stream is not None:
+        if stream.device != t.device:
+            raise ValueError(f"stream of {stream.device} for tensors on {t.device}")
+        return torch.cuda.stream(stream)
+    return _NO_GUARD if torch.cuda.current_device() == t.device.index else torch.cuda.device(t.device)
+
+
+def _on(dev, t: torch.Tensor | None, dtype, shape, name: str) -> int | None:
+    """The address of t, checked to be a contiguous dtype tensor of `shape` on `dev`; None for None."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
+        raise ValueError(f"{name}: expected contiguous {dtype} {tuple(shape)} on {dev}, "
+                         f"got {t.dtype} {tuple(t.shape)} on {t.device}"
+                         f"{'' if t.is_contiguous() else ', not contiguous'}")
+    return t.data_ptr()
+
+
+def _out(dev, t: torch.Tensor | None, dtype, shape, name: str, want: bool = True):
+    """An output: t, checked, or a new tensor where one is wanted."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=dev) if want else None
+    _on(dev, t, dtype, shape, name)
+    return t
+
+
+def _scratch(dev, ws: torch.Tensor | None, nbytes: int) -> torch.Tensor:
+    if ws is None:
+        return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
+    _on(dev, ws, torch.uint8, ws.shape, "ws")
+    return ws
+
+
+def _matrix(t: torch.Tensor, name: str):
+    if t.dim() != 2:
+        raise ValueError(f"{name}: expected a 2-D tensor, got {tuple(t.shape)}")
+    return t.shape
+
+
+ACT_NONE, ACT_RELU, ACT_GELU, ACT_GELU_TANH, ACT_SILU = 0, 1, 2, 3, 4
+ACTIVATIONS = {"none": ACT_NONE, "relu": ACT_RELU, "gelu": ACT_GELU, "gelu_tanh": ACT_GELU_TANH,
+               "silu": ACT_SILU}
+
+
+def _act_id(act) -> int:
+    """An activation's id from its name or id (the library checks ids)."""
+    if isinstance(act, str):
+        if act not in ACTIVATIONS:
+            raise ValueError(f"unknown activation {act!r}: one of {', '.join(ACTIVATIONS)}")
+        return ACTIVATIONS[act]
+    return int(act)
+
+
+def qlora_linear_fwd_epilogue(X: torch.Tensor, p: PackedNF4, L1: torch.Tensor, L2: torch.Tensor,
+                              s: float, bias: torch.Tensor | None = None, act="none",
+                              residual: torch.Tensor | None = None, Y: torch.Tensor | None = None,
+                              Z: torch.Tensor | None = None, want_Z: bool = False,
+                              sT: torch.Tensor | None = None, want_sT: bool = True,
+                              ws: torch.Tensor | None = None, stream=None):
+    """Z = X.W' + s.X.L1.L2 + bias, Y = act(Z) + residual. act: a name of ACTIVATIONS or its id.
+    residual may be Y itself. Returns (Y t x o bf16, Z t x o bf16 or None, sT t x r bf16 or None);
+    keep Z for qlora_epilogue_bwd and sT for qlora_linear_bwd."""
+    (t, h), (_, r), o, dev = _matrix(X, "X"), _matrix(L1, "L1"), p.out_features, X.device
+    with _guard(X, stream):
+        if h != p.in_features:
+            raise ValueError("X and W disagree on in_features")
+        if p.codes.device != dev:
+            raise ValueError(f"the packed weight is on {p.codes.device}, X on {dev}")
+        bf16 = torch.bfloat16
+        ins = (_on(dev, X, bf16, (t, h), "X"), _on(dev, L1, bf16, (h, r), "L1"),
+               _on(dev, L2, bf16, (r, o), "L2"), _on(dev, bias, bf16, (o,), "bias"),
+               _on(dev, residual, bf16, (t, o), "residual"))
+        Y = _out(dev, Y, bf16, (t, o), "Y")
+        Z = _out(dev, Z, bf16, (t, o), "Z", want_Z)
+        sT = _out(dev, sT, bf16, (t, r), "sT", want_sT)
+        ws = _scratch(dev, ws, fwd_workspace_bytes(t, h, o, r))
+        d = p.desc()
+        _check(lib().qlora_linear_fwd_epilogue(
+            ins[0], t, ctypes.byref(d), ins[1], ins[2], r, float(s), ins[3], _act_id(act), ins[4],
+            Y.data_ptr(), _ptr(Z), _ptr(sT), ws.data_ptr(), ws.numel(), _stream()),
+            "qlora_linear_fwd_epilogue")
+    return Y, Z, sT
+
+
+def qlora_epilogue_bwd(dY: torch.Tensor, Z: torch.Tensor | None, act="none",
+                       dZ: torch.Tensor | None = None, dbias: torch.Tensor | None = None,
+                       want_dZ: bool = True, want_dbias: bool = True,
+                       ws: torch.Tensor | None = None, stream=None):
+    """dZ = dY . act'(Z) (bf16) and dbias = its sum over tokens (fp32), either one None if not
+    wanted. Pass dZ on to qlora_linear_bwd; the residual's gradient is dY. dZ may be dY itself."""
+    (t, o), dev = _matrix(dY, "dY"), dY.device
+    with _guard(dY, stream):
+        a, z = (_on(dev, x, torch.bfloat16, (t, o), n) for x, n in ((dY, "dY"), (Z, "Z")))
+        dZ = _out(dev, dZ, torch.bfloat16, (t, o), "dZ", want_dZ)
+        dbias = _out(dev, dbias, torch.float32, (o,), "dbias", want_dbias)
+        if dbias is not None:
+            ws = _scratch(dev, ws, int(lib().qlora_epilogue_bwd_workspace_bytes(t, o)))
+        _check(lib().qlora_epilogue_bwd(a, z, t, o, _act_id(act), _ptr(dZ), _ptr(dbias), _ptr(ws),
+                                        0 if ws is None else ws.numel(), _stream()),
+               "qlora_epilogue_bwd")
+    return dZ, dbias
+
+
+def _gate_shape(gate: torch.Tensor | None, rows_per_gate, t: int, h: int):
+    """(rows_per_gate, the gate's shape): one row for all tokens unless rows_per_gate is given."""
+    if gate is None:
+        return 0, None
+    rows = t if rows_per_gate is None else int(rows_per_gate)
+    return rows, (-(-t // rows) if rows > 0 else 0, h)
+
+
+def qlora_norm_residual_fwd(x: torch.Tensor, y: torch.Tensor | None = None,
+                            w_post: torch.Tensor | None = None, gate: torch.Tensor | None = None,
+                            w_pre: torch.Tensor | None = None, scale: float = 1.0, eps: float = 1e-6,
+                            rows_per_gate: int | None = None, x_out: torch.Tensor | None = None,
+                            n: torch.Tensor | None = None, want_rstd: bool = True, stream=None):
+    """u = y.rstd(y).w_post, x' = x + scale.gate.u, n = x'.rstd(x').w_pre; without y, x' = x.
+    gate: ceil(t / rows_per_gate) rows of h (one for all tokens by default). Returns
+    (x' t x h bf16, n t x h bf16 or None, rstd_post t fp32 or None, rstd_pre t fp32 or None)."""
+    (t, h), dev, bf16 = _matrix(x, "x"), x.device, torch.bfloat16
+    rows, gshape = _gate_shape(gate, rows_per_gate, t, h)
+    with _guard(x, stream):
+        xp, yp = _on(dev, x, bf16, (t, h), "x"), _on(dev, y, bf16, (t, h), "y")
+        wo, gp = _on(dev, w_post, bf16, (h,), "w_post"), _on(dev, gate, bf16, gshape, "gate")
+        wi = _on(dev, w_pre, bf16, (h,), "w_pre")
+        x_out = _out(dev, x_out, bf16, (t, h), "x_out")
+        n = _out(dev, n, bf16, (t, h), "n", w_pre is not None)
+        ro = torch.empty(t, dtype=torch.float32, device=dev) if want_rstd and wo else None
+        ri = torch.empty(t, dtype=torch.float32, device=dev) if want_rstd and wi else None
+        _check(lib().qlora_norm_residual_fwd(xp, yp, t, h, wo, gp, rows, float(scale), wi, float(eps),
+                                             x_out.data_ptr(), _ptr(n), _ptr(ro), _ptr(ri), _stream()),
+               "qlora_norm_residual_fwd")
+    return x_out, n, ro, ri
+
+
+def qlora_norm_residual_bwd(dx_out: torch.Tensor | None, dn: torch.Tensor | None, x_out: torch.Tensor | None,
+                            y: torch.Tensor | None, rstd_post: torch.Tensor | None,
+                            rstd_pre: torch.Tensor | None, w_post: torch.Tensor | None = None,
+                            gate: torch.Tensor | None = None, w_pre: torch.Tensor | None = None,
+                            scale: float = 1.0, rows_per_gate: int | None = None,
+                            ws: torch.Tensor | None = None, stream=None):
+    """Gradients of qlora_norm_residual_fwd from those of x' and n (either may be None: zero), with
+    the forward's x', y, rstd_post and rstd_pre. Returns (dx t x h bf16, dy t x h bf16, dw_post h
+    fp32, dgate fp32 of the gate's shape, dw_pre h fp32), None where there is no such input."""
+    like = dx_out if dx_out is not None else dn
+    if like is None:
+        raise ValueError("one of dx_out and dn is needed")
+    (t, h), dev, bf16, f32 = _matrix(like, "dx_out or dn"), like.device, torch.bfloat16, torch.float32
+    rows, gshape = _gate_shape(gate, rows_per_gate, t, h)
+    with _guard(like, stream):
+        if dn is None:      # n's gradient is zero: nothing of the second norm is needed
+            x_out = rstd_pre = w_pre_used = None
+        else:
+            w_pre_used = w_pre
+        g = [_on(dev, v, bf16, (t, h), s) for v, s in ((dx_out, "dx_out"), (dn, "dn"), (x_out, "x_out"), (y, "y"))]
+        wo, gp = _on(dev, w_post, bf16, (h,), "w_post"), _on(dev, gate, bf16, gshape, "gate")
+        wi = _on(dev, w_pre_used, bf16, (h,), "w_pre")
+        ro, ri = _on(dev, rstd_post, f32, (t,), "rstd_post"), _on(dev, rstd_pre, f32, (t,), "rstd_pre")
+        dx = torch.empty(t, h, dtype=bf16, device=dev)
+        dy = torch.empty(t, h, dtype=bf16, device=dev) if y is not None else None
+        dwo = torch.empty(h, dtype=f32, device=dev) if wo else None
+        dg = torch.empty(gshape, dtype=f32, device=dev) if gp else None
+        dwi = torch.empty(h, dtype=f32, device=dev) if wi else None
+        ws = _scratch(dev, ws, int(lib().qlora_norm_residual_bwd_workspace_bytes(t, h)))
+        _check(lib().qlora_norm_residual_bwd(*g, t, h, wo, gp, rows, float(scale), wi, ro, ri, dx.data_ptr(),
+                                             _ptr(dy), _ptr(dwo), _ptr(dg), _ptr(dwi), ws.data_ptr(),
+                                             ws.numel(), _stream()),
+               "qlora_norm_residual_bwd")
+        if dn is None and w_pre is not None:
+            dwi = torch.zeros(h, dtype=f32, device=dev)
+    return dx, dy, dwo, dg, dwi
 
 
 class KernelProfile:

@@ -1,0 +1,280 @@
+// Host side of the operators around the linear: the fused epilogue, the norms of a block with its
+// gate and residual scale. Included by qlora_nf4.cu, whose argument checks, device table and launch
+// helpers it uses.
+#pragma once
+
+namespace {
+
+// ------------------------------------------------------------------------------------------
+// the linear's epilogue
+// ------------------------------------------------------------------------------------------
+bool valid_act(int act) { return act >= QLORA_ACT_NONE && act <= QLORA_ACT_SILU; }
+static_assert(kActNone == QLORA_ACT_NONE && kActRelu == QLORA_ACT_RELU && kActGelu == QLORA_ACT_GELU &&
+              kActGeluTanh == QLORA_ACT_GELU_TANH && kActSilu == QLORA_ACT_SILU, "activation ids");
+
+// Runs of rows of the epilogue's backward: one wave of CTAs over the card, each with at least two
+// rounds of its warps' rows in flight, so that a short batch is not cut into runs whose partial sums
+// cost more than they save. The workspace is sized for the most runs there can be (sms = 0).
+constexpr int kMaxEpiRuns = 1024;
+int epilogue_runs(int64_t t, int64_t o, int sms, int ctas) {
+  const int64_t rows = 2 * ep::kUnroll * ep::kWarps;
+  int64_t runs = std::min<int64_t>((t + rows - 1) / rows, kMaxEpiRuns);
+  const int64_t blocks = (o + ep::kCols - 1) / ep::kCols;
+  if (sms) runs = std::min(runs, std::max<int64_t>(1, static_cast<int64_t>(sms) * ctas / blocks));
+  return static_cast<int>(runs);
+}
+
+cudaError_t launch_finish(const float* part_pre, const float* part_post, const float* part_gate, float* dw_pre,
+                          float* dw_post, float* dgate, int t, int h, int rows_per_gate, int parts, int units,
+                          int grid_y, cudaStream_t st) {
+  dim3 grid(static_cast<unsigned>((h + nr::kFinishCols - 1) / nr::kFinishCols), static_cast<unsigned>(grid_y));
+  norm_residual_finish_kernel<<<grid, nr::kFinishWarps * 32, 0, st>>>(
+      part_pre, part_post, part_gate, dw_pre, dw_post, dgate, t, h, rows_per_gate, parts, units);
+  return cudaGetLastError();
+}
+
+// ------------------------------------------------------------------------------------------
+// norms
+// ------------------------------------------------------------------------------------------
+int check_norm_shape(int64_t t, int64_t h) {
+  if (t < 1) return QLORA_ERR_INVALID_ARG;
+  if (h < 8 || h % 8 != 0 || h > nr::kMaxH || t >= kMaxDim) return QLORA_ERR_BAD_SHAPE;
+  return QLORA_OK;
+}
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+struct NormBwdPlan {
+  int threads, ctas, units;   // CTAs, and runs of rows (warps for short rows, else CTAs)
+  size_t smem;
+};
+constexpr int kNormCtasPerSm = 4;
+NormBwdPlan plan_norm_bwd(int64_t t, int64_t h, int sms) {
+  NormBwdPlan p{};
+  if (h <= nr::kWarpRowH) {
+    constexpr int wpc = nr::kWarpRowThreads / 32;
+    p.threads = nr::kWarpRowThreads;
+    p.ctas = static_cast<int>(std::min<int64_t>((t + wpc - 1) / wpc, static_cast<int64_t>(sms) * 2));
+    p.units = p.ctas * wpc;
+    p.smem = static_cast<size_t>(wpc) * h * 4;
+  } else {
+    const int64_t vecs = h / 8;
+    const bool two = vecs > 1024;
+    p.threads = static_cast<int>(((two ? (vecs + 1) / 2 : vecs) + 31) / 32 * 32);
+    // as many CTAs as an SM's threads hold at the kernel's 64 registers a thread
+    const int per_sm = two ? 1 : std::max(1, std::min(kNormCtasPerSm, 1024 / p.threads));
+    p.ctas = static_cast<int>(std::min<int64_t>(t, static_cast<int64_t>(sms) * per_sm));
+    p.units = p.ctas;
+    p.smem = two ? static_cast<size_t>(h) * 3 * 4 : 0;
+  }
+  return p;
+}
+
+constexpr int kMaxSms = 160;   // workspace sizes are host functions: sized for any B200
+
+}  // namespace
+
+extern "C" {
+
+int qlora_linear_fwd_epilogue(const uint16_t* X, int64_t t, const nf4_weight* W, const uint16_t* L1,
+                              const uint16_t* L2, int64_t r, float s, const uint16_t* bias, int act,
+                              const uint16_t* residual, uint16_t* Y, uint16_t* Z_out, uint16_t* sT_out,
+                              void* workspace, size_t ws_bytes, qlora_stream_t stream) {
+  int rc = check_fwd_args(X, t, W, L1, L2, r, s, Y, sT_out, workspace);
+  if (rc) return rc;
+  if (!valid_act(act)) return QLORA_ERR_INVALID_ARG;
+  if ((bias && !aligned16(bias)) || (residual && !aligned16(residual)) || (Z_out && !aligned16(Z_out)))
+    return QLORA_ERR_MISALIGNED;
+  if (!workspace || ws_bytes < qlora_fwd_workspace_bytes(t, W->in_features, W->out_features, r))
+    return QLORA_ERR_WORKSPACE;
+  EpilogueArgs e{};
+  e.bias = bias;
+  e.residual = residual;
+  e.z_out = Z_out;
+  e.act = act;
+  return fwd_core(X, X, t, W, L1, L2, r, s, Y, sT_out, workspace, reinterpret_cast<cudaStream_t>(stream), &e);
+}
+
+size_t qlora_epilogue_bwd_workspace_bytes(int64_t t, int64_t o) {
+  if (t < 1 || t >= kMaxDim || o < 8 || o % 8 != 0 || o >= kMaxDim) return 0;
+  return align256(static_cast<size_t>(epilogue_runs(t, o, 0, 0)) * o * 4);
+}
+
+int qlora_epilogue_bwd(const uint16_t* dY, const uint16_t* Z, int64_t t, int64_t o, int act, uint16_t* dZ,
+                       float* dbias, void* workspace, size_t ws_bytes, qlora_stream_t stream) {
+  if (!dY || !valid_act(act) || (!dZ && !dbias) || (act != QLORA_ACT_NONE && !Z) || t < 1)
+    return QLORA_ERR_INVALID_ARG;
+  if (o < 8 || o % 8 != 0 || o >= kMaxDim || t >= kMaxDim) return QLORA_ERR_BAD_SHAPE;
+  if (!aligned16(dY) || (Z && !aligned16(Z)) || (dZ && !aligned16(dZ)) || (dbias && !aligned16(dbias)) ||
+      (workspace && !aligned16(workspace)))
+    return QLORA_ERR_MISALIGNED;
+  if (dbias && (!workspace || ws_bytes < qlora_epilogue_bwd_workspace_bytes(t, o))) return QLORA_ERR_WORKSPACE;
+  int dev, rc;
+  if ((rc = current_device(&dev))) return rc;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const int runs = epilogue_runs(t, o, sm_count(dev), device_info(dev).epi_bwd_ctas);
+  EpilogueBwdArgs a{};
+  a.dY = dY;
+  a.Z = Z;
+  a.dZ = dZ;
+  a.part = !dbias ? nullptr : (runs == 1 ? dbias : reinterpret_cast<float*>(workspace));
+  a.t = t;
+  a.o = static_cast<int>(o);
+  dim3 grid(static_cast<unsigned>((o + ep::kCols - 1) / ep::kCols), static_cast<unsigned>(runs));
+  {
+    prof::Scope ps(prof::kEpilogueBwd, st);
+    switch (act) {
+      case QLORA_ACT_RELU: epilogue_bwd_kernel<kActRelu><<<grid, ep::kWarps * 32, 0, st>>>(a); break;
+      case QLORA_ACT_GELU: epilogue_bwd_kernel<kActGelu><<<grid, ep::kWarps * 32, 0, st>>>(a); break;
+      case QLORA_ACT_GELU_TANH: epilogue_bwd_kernel<kActGeluTanh><<<grid, ep::kWarps * 32, 0, st>>>(a); break;
+      case QLORA_ACT_SILU: epilogue_bwd_kernel<kActSilu><<<grid, ep::kWarps * 32, 0, st>>>(a); break;
+      default: epilogue_bwd_kernel<kActNone><<<grid, ep::kWarps * 32, 0, st>>>(a); break;
+    }
+  }
+  if ((rc = launch_status())) return rc;
+  if (dbias && runs > 1 &&
+      launch_finish(a.part, nullptr, nullptr, dbias, nullptr, nullptr, static_cast<int>(t), a.o, 1, runs, 0, 1,
+                    st) != cudaSuccess)
+    return QLORA_ERR_CUDA;
+  return QLORA_OK;
+}
+
+int qlora_norm_residual_fwd(const uint16_t* x, const uint16_t* y, int64_t t, int64_t h, const uint16_t* w_post,
+                            const uint16_t* gate, int64_t rows_per_gate, float scale, const uint16_t* w_pre,
+                            float eps, uint16_t* x_out, uint16_t* n_out, float* rstd_post, float* rstd_pre,
+                            qlora_stream_t stream) {
+  if (!x || (!y && (w_post || gate)) || !w_pre != !n_out || (!x_out && !n_out) || (rstd_post && !w_post) ||
+      (rstd_pre && !w_pre) || (gate && rows_per_gate < 1) || !std::isfinite(scale) || !std::isfinite(eps) ||
+      eps < 0.f)
+    return QLORA_ERR_INVALID_ARG;
+  int rc = check_norm_shape(t, h);
+  if (rc) return rc;
+  for (const void* p : {static_cast<const void*>(x), static_cast<const void*>(y), static_cast<const void*>(w_post),
+                        static_cast<const void*>(gate), static_cast<const void*>(w_pre),
+                        static_cast<const void*>(x_out), static_cast<const void*>(n_out)})
+    if (p && !aligned16(p)) return QLORA_ERR_MISALIGNED;
+  if (!aligned4(rstd_post) || !aligned4(rstd_pre)) return QLORA_ERR_MISALIGNED;
+  int dev;
+  if ((rc = current_device(&dev))) return rc;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  NormFwdArgs a{};
+  a.x = x;
+  a.y = y;
+  a.w_post = w_post;
+  a.gate = gate;
+  a.w_pre = w_pre;
+  a.x_out = x_out;
+  a.n_out = n_out;
+  a.rstd_post = rstd_post;
+  a.rstd_pre = rstd_pre;
+  a.t = static_cast<int>(t);
+  a.h = static_cast<int>(h);
+  a.rows_per_gate = static_cast<int>(gate ? std::min(rows_per_gate, t) : t);
+  a.scale = scale;
+  a.eps = eps;
+  {
+    prof::Scope ps(prof::kNorm, st);
+    if (h <= nr::kWarpRowH) {
+      constexpr int wpc = nr::kWarpRowThreads / 32;
+      const unsigned grid = static_cast<unsigned>((t + wpc - 1) / wpc);
+      if (h <= 256)
+        norm_residual_fwd_kernel<1, true><<<grid, nr::kWarpRowThreads, 0, st>>>(a);
+      else
+        norm_residual_fwd_kernel<2, true><<<grid, nr::kWarpRowThreads, 0, st>>>(a);
+    } else {
+      // vectors of 8 per thread: one while the card has threads to spare for the rows there are
+      // (a shorter way through the row), else two, which keeps more loads of a thread in flight
+      const int64_t vecs = h / 8;
+      const bool two = vecs > 1024 || (vecs >= 256 && t >= 2 * sm_count(dev));
+      const unsigned threads = static_cast<unsigned>(((two ? (vecs + 1) / 2 : vecs) + 31) / 32 * 32);
+      const unsigned grid = static_cast<unsigned>(t);
+      if (two)
+        norm_residual_fwd_kernel<2, false><<<grid, threads, 0, st>>>(a);
+      else
+        norm_residual_fwd_kernel<1, false><<<grid, threads, 0, st>>>(a);
+    }
+  }
+  return launch_status();
+}
+
+size_t qlora_norm_residual_bwd_workspace_bytes(int64_t t, int64_t h) {
+  if (check_norm_shape(t, h) != QLORA_OK) return 0;
+  const NormBwdPlan p = plan_norm_bwd(t, h, kMaxSms);
+  return 2 * align256(static_cast<size_t>(p.ctas) * h * 4) + align256(2 * static_cast<size_t>(p.units) * h * 4);
+}
+
+int qlora_norm_residual_bwd(const uint16_t* dx_out, const uint16_t* dn, const uint16_t* x_out, const uint16_t* y,
+                            int64_t t, int64_t h, const uint16_t* w_post, const uint16_t* gate,
+                            int64_t rows_per_gate, float scale, const uint16_t* w_pre, const float* rstd_post,
+                            const float* rstd_pre, uint16_t* dx, uint16_t* dy, float* dw_post, float* dgate,
+                            float* dw_pre, void* workspace, size_t ws_bytes, qlora_stream_t stream) {
+  if (!dx || (!dx_out && !dn) || !dn != !w_pre || !dn != !dw_pre || (dn && (!x_out || !rstd_pre)) || !y != !dy ||
+      (!y && (w_post || gate)) || !w_post != !dw_post || (w_post && !rstd_post) || !gate != !dgate ||
+      (gate && rows_per_gate < 1) || !std::isfinite(scale))
+    return QLORA_ERR_INVALID_ARG;
+  int rc = check_norm_shape(t, h);
+  if (rc) return rc;
+  for (const void* p :
+       {static_cast<const void*>(dx_out), static_cast<const void*>(dn), static_cast<const void*>(x_out),
+        static_cast<const void*>(y), static_cast<const void*>(w_post), static_cast<const void*>(gate),
+        static_cast<const void*>(w_pre), static_cast<const void*>(dx), static_cast<const void*>(dy),
+        static_cast<const void*>(dw_post), static_cast<const void*>(dgate), static_cast<const void*>(dw_pre),
+        static_cast<const void*>(workspace)})
+    if (p && !aligned16(p)) return QLORA_ERR_MISALIGNED;
+  if (!aligned4(rstd_post) || !aligned4(rstd_pre)) return QLORA_ERR_MISALIGNED;
+  if (!workspace || ws_bytes < qlora_norm_residual_bwd_workspace_bytes(t, h)) return QLORA_ERR_WORKSPACE;
+  int dev;
+  if ((rc = current_device(&dev))) return rc;
+  if (sm_count(dev) > kMaxSms) return QLORA_ERR_UNSUPPORTED_DEVICE;
+  cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  const NormBwdPlan pl = plan_norm_bwd(t, h, sm_count(dev));
+  uint8_t* ws = reinterpret_cast<uint8_t*>(workspace);
+  const size_t part = align256(static_cast<size_t>(pl.ctas) * h * 4);
+  NormBwdArgs a{};
+  a.dx_out = dx_out;
+  a.dn = dn;
+  a.x_out = x_out;
+  a.y = y;
+  a.w_post = w_post;
+  a.gate = gate;
+  a.w_pre = w_pre;
+  a.rstd_post = rstd_post;
+  a.rstd_pre = rstd_pre;
+  a.dx = dx;
+  a.dy = dy;
+  a.dw_post = dw_post;
+  a.dgate = dgate;
+  a.dw_pre = dw_pre;
+  a.part_post = pl.ctas == 1 ? dw_post : reinterpret_cast<float*>(ws);
+  a.part_pre = pl.ctas == 1 ? dw_pre : reinterpret_cast<float*>(ws + part);
+  a.part_gate = reinterpret_cast<float*>(ws + 2 * part);
+  a.t = static_cast<int>(t);
+  a.h = static_cast<int>(h);
+  a.rows_per_gate = static_cast<int>(gate ? std::min(rows_per_gate, t) : t);
+  a.units = pl.units;
+  a.scale = scale;
+  {
+    prof::Scope ps(prof::kNorm, st);
+    const unsigned grid = static_cast<unsigned>(pl.ctas), threads = static_cast<unsigned>(pl.threads);
+    if (h <= 256)
+      norm_residual_bwd_kernel<1, true><<<grid, threads, pl.smem, st>>>(a);
+    else if (h <= nr::kWarpRowH)
+      norm_residual_bwd_kernel<2, true><<<grid, threads, pl.smem, st>>>(a);
+    else if (h <= 8192)
+      norm_residual_bwd_kernel<1, false><<<grid, threads, pl.smem, st>>>(a);
+    else
+      norm_residual_bwd_kernel<2, false><<<grid, threads, pl.smem, st>>>(a);
+  }
+  if ((rc = launch_status())) return rc;
+  // gate rows are shared between units unless every unit's run starts a new one
+  const int gate_blocks = gate && a.rows_per_gate > 1 && pl.units > 1 ? std::min(16, (pl.units + 6) / 8) : 0;
+  float* pre = pl.ctas > 1 ? dw_pre : nullptr;
+  float* post = pl.ctas > 1 ? dw_post : nullptr;
+  if (!pre && !post && !gate_blocks) return QLORA_OK;
+  if (launch_finish(a.part_pre, a.part_post, a.part_gate, pre, post, dgate, a.t, a.h, a.rows_per_gate, pl.ctas,
+                    pl.units, 2 + gate_blocks, st) != cudaSuccess)
+    return QLORA_ERR_CUDA;
+  return QLORA_OK;
+}
+
+}  // extern "C"

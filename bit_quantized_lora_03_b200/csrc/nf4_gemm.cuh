@@ -25,6 +25,7 @@
 // stops issuing, waits for its own copies and MMAs in flight, frees TMEM and returns.
 #pragma once
 
+#include "epilogue.cuh"
 #include "nf4_codec.cuh"
 
 namespace qlora {
@@ -49,6 +50,8 @@ constexpr int kTmaWarp = 8;
 constexpr int kMmaWarp = 9;                // even CTA: MMA issuer; odd CTA: readiness relay
 constexpr int kThreads = 10 * 32;
 constexpr int kTmemCols = 512;
+constexpr int kEpiZTile = kWorkWarps * 8192;   // the staging tiles of Z lie behind those of Y
+static_assert(2 * kEpiZTile <= STAGES * (A_BYTES + B_BYTES), "staging tiles in the drained stage buffers");
 
 constexpr size_t nf4_gemm_smem_bytes() {
   return 1024 /* alignment slack */ + STAGES * (A_BYTES + B_BYTES + P_BYTES) + 256;
@@ -68,6 +71,7 @@ struct Nf4GemmArgs {
   Nf4Table tab;
   const uint16_t* addend;  // NULL, or M x N bf16 added to the accumulator before the rounding;
                            // written by the previous kernel on the stream (waited for first)
+  EpilogueArgs epi;        // kEpi only
 };
 
 // Wait for an mbarrier phase ignoring the abort flag (used only to drain in-flight copies
@@ -82,12 +86,15 @@ __device__ __forceinline__ void mbar_drain(uint64_t* bar, uint32_t parity) {
   }
 }
 
-template <bool kBwd>
+// kEpi: Z = accumulator + bias, Y = act(Z) + residual instead of the plain rounding; Z is stored
+// through tmZ where the caller keeps it.
+template <bool kBwd, bool kEpi = false>
 __global__ void __launch_bounds__(tc::kThreads, 1)
     nf4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmP,
                     const __grid_constant__ CUtensorMap tmA2,
                     const __grid_constant__ CUtensorMap tmB2,
-                    const __grid_constant__ CUtensorMap tmOut, const Nf4GemmArgs args) {
+                    const __grid_constant__ CUtensorMap tmOut, const __grid_constant__ CUtensorMap tmZ,
+                    const Nf4GemmArgs args) {
   using namespace tc;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -360,6 +367,41 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
                                              __uint_as_float(w[k] & 0xFFFF0000u));
             }
           }
+          uint8_t* rowp = buf + lane * 128;
+          if (kEpi) {
+            const int col = n0 + (c0 + q) * 16;
+            float z[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) z[k] = __uint_as_float(v[k]);
+            if (args.epi.bias) {
+#pragma unroll
+              for (int g = 0; g < 2; ++g) {
+                float b[8];
+                unpack8(ldg_vec(args.epi.bias, (col >> 3) + g), b);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) z[8 * g + k] += b[k];
+              }
+            }
+            if (args.epi.z_out) {
+#pragma unroll
+              for (int g = 0; g < 2; ++g)
+                *reinterpret_cast<uint4*>(rowp + kEpiZTile + (((2 * q + g) ^ (lane & 7)) << 4)) =
+                    make_uint4(pack_bf16x2(z[8 * g], z[8 * g + 1]), pack_bf16x2(z[8 * g + 2], z[8 * g + 3]),
+                               pack_bf16x2(z[8 * g + 4], z[8 * g + 5]), pack_bf16x2(z[8 * g + 6], z[8 * g + 7]));
+            }
+            act_apply(z, args.epi.act);
+            if (args.epi.residual && row < args.M) {
+#pragma unroll
+              for (int g = 0; g < 2; ++g) {
+                float b[8];
+                unpack8(ldg_vec(args.epi.residual, ((static_cast<int64_t>(row) * args.N + col) >> 3) + g), b);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) z[8 * g + k] += b[k];
+              }
+            }
+#pragma unroll
+            for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(z[k]);
+          }
           uint4 o0, o1;
           o0.x = pack_bf16x2(__uint_as_float(v[0]), __uint_as_float(v[1]));
           o0.y = pack_bf16x2(__uint_as_float(v[2]), __uint_as_float(v[3]));
@@ -369,7 +411,6 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
           o1.y = pack_bf16x2(__uint_as_float(v[10]), __uint_as_float(v[11]));
           o1.z = pack_bf16x2(__uint_as_float(v[12]), __uint_as_float(v[13]));
           o1.w = pack_bf16x2(__uint_as_float(v[14]), __uint_as_float(v[15]));
-          uint8_t* rowp = buf + lane * 128;
           *reinterpret_cast<uint4*>(rowp + (((2 * q) ^ (lane & 7)) << 4)) = o0;
           *reinterpret_cast<uint4*>(rowp + (((2 * q + 1) ^ (lane & 7)) << 4)) = o1;
         }
@@ -377,6 +418,7 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
         __syncwarp();
         if (lane == 0 && any_row) {
           tma_store_2d(&tmOut, buf, n0 + c0 * 16, row0);
+          if (kEpi && args.epi.z_out) tma_store_2d(&tmZ, buf + kEpiZTile, n0 + c0 * 16, row0);
           bulk_commit_group();
         }
       }

@@ -28,6 +28,7 @@
 // cluster of 8 CTAs launched just before, which also zeroes the fp32 buffer and the counters.
 #pragma once
 
+#include "epilogue.cuh"
 #include "nf4_codec.cuh"
 
 namespace qlora {
@@ -95,6 +96,7 @@ struct GemvArgs {
   int t;
   int r;
   Nf4Table tab;
+  EpilogueArgs epi;    // kEpi only
 };
 
 __device__ __forceinline__ void mma_bf16_16816(float (&d)[4], uint32_t a0, uint32_t a1,
@@ -282,7 +284,7 @@ __device__ __forceinline__ void gemv_flush(float (&acc)[2][NT][4], const GemvArg
 // The last warp to add to a row tile finishes it: Y[n][row] = bf16(Y32[n][row] + sum_c
 // sT[n][c] L2[c][row]) for its 32 rows, lane = row. The fp32 sums of the other warps are read
 // from L2 after the counter showed them all done (each adder fenced before counting).
-template <int NT>
+template <int NT, bool kEpi>
 __device__ __forceinline__ void gemv_finish_tile(const GemvArgs& a, const uint16_t* sts,
                                                  int64_t tile, int lane) {
   const int64_t row = tile * gv::kTileRows + lane;
@@ -301,13 +303,27 @@ __device__ __forceinline__ void gemv_finish_tile(const GemvArgs& a, const uint16
       for (int n = 0; n < NT * 8; ++n)
         if (n < a.t) y[n] = fmaf(bf16_bits_to_float(sts[n * gv::kMaxRank + c0 + j]), l2[j], y[n]);
   }
+  if (kEpi) {   // Z = y + b, Y = act(Z) + R; lane = row of Wt: 64-byte pieces of a token's row
+    const float b = a.epi.bias ? bf16_bits_to_float(__ldg(a.epi.bias + row)) : 0.f;
+#pragma unroll
+    for (int n = 0; n < NT * 8; ++n) {
+      y[n] += b;
+      if (n < a.t && a.epi.z_out)
+        a.epi.z_out[static_cast<int64_t>(n) * a.o + row] = __bfloat16_as_ushort(__float2bfloat16_rn(y[n]));
+    }
+    act_apply(y, a.epi.act);
+#pragma unroll
+    for (int n = 0; n < NT * 8; ++n)
+      if (n < a.t && a.epi.residual)
+        y[n] += bf16_bits_to_float(__ldg(a.epi.residual + static_cast<int64_t>(n) * a.o + row));
+  }
 #pragma unroll
   for (int n = 0; n < NT * 8; ++n)
     if (n < a.t)
       a.Y[static_cast<int64_t>(n) * a.o + row] = __bfloat16_as_ushort(__float2bfloat16_rn(y[n]));
 }
 
-template <int NT>  // NT: n8 token tiles (1 for t <= 8, 2 for t <= 16)
+template <int NT, bool kEpi = false>  // NT: n8 token tiles (1 for t <= 8, 2 for t <= 16)
 __global__ void __launch_bounds__(gv::kThreads, 1)
     nf4_gemv_kernel(const GemvArgs args, const __grid_constant__ CUtensorMap map_codes) {
   using namespace gv;
@@ -477,7 +493,7 @@ __global__ void __launch_bounds__(gv::kThreads, 1)
       before_me = __shfl_sync(0xffffffffu, before_me, 0);
       if (before_me + tile_units == upt) {
         __threadfence();
-        gemv_finish_tile<NT>(args, sts, cur.tile, lane);
+        gemv_finish_tile<NT, kEpi>(args, sts, cur.tile, lane);
       }
       tile_units = 0;
     }

@@ -21,6 +21,8 @@
 #include "adamw.cuh"
 #include "dropout.cuh"
 #include "nf4_gemv.cuh"
+#include "norm_residual.cuh"
+#include "epilogue.cuh"
 
 using namespace qlora;
 
@@ -143,6 +145,14 @@ Nf4Buckets device_buckets(int id = 0) {
 // ------------------------------------------------------------------------------------------
 // device checks, kernel attributes
 // ------------------------------------------------------------------------------------------
+// Shared-memory limits of the kernels launched from block_ops.cuh.
+bool block_ops_attributes() {
+  bool fine = true;
+  fine &= cudaFuncSetAttribute(norm_residual_bwd_kernel<2, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               nr::kMaxH * 3 * 4) == cudaSuccess;
+  return fine;
+}
+
 constexpr int kMaxDevices = 64;
 
 struct DeviceInfo {
@@ -154,6 +164,7 @@ struct DeviceInfo {
   int dq_ctas = 1;           // nf4_dequantize_kernel
   int adamw_ctas = 1;        // adamw_kernel, 256 threads
   int adamw_multi_ctas = 1;  // adamw_multi_kernel, 256 threads
+  int epi_bwd_ctas = 1;      // epilogue_bwd_kernel, the widest of its variants
 };
 DeviceInfo g_dev[kMaxDevices];
 
@@ -184,6 +195,13 @@ int current_device(int* dev_out) {
                                  static_cast<int>(tc::nf4_gemm_smem_bytes())) == cudaSuccess;
     fine &= cudaFuncSetAttribute(nf4_gemm_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  static_cast<int>(tc::nf4_gemm_smem_bytes())) == cudaSuccess;
+    fine &= cudaFuncSetAttribute(nf4_gemm_kernel<false, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 static_cast<int>(tc::nf4_gemm_smem_bytes())) == cudaSuccess;
+    fine &= cudaFuncSetAttribute(nf4_gemv_kernel<1, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 static_cast<int>(gv::smem_bytes())) == cudaSuccess;
+    fine &= cudaFuncSetAttribute(nf4_gemv_kernel<2, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 static_cast<int>(gv::smem_bytes())) == cudaSuccess;
+    fine &= block_ops_attributes();
     fine &= cudaFuncSetAttribute(nf4_quantize_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  static_cast<int>(qz::smem_bytes())) == cudaSuccess;
     fine &= cudaFuncSetAttribute(gemv_lora_down_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -216,6 +234,10 @@ int current_device(int* dev_out) {
     n = 0;
     fine &= cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, adamw_multi_kernel, 256, 0) == cudaSuccess;
     d.adamw_multi_ctas = std::max(1, n);
+    n = 0;
+    fine &= cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, epilogue_bwd_kernel<kActGelu>,
+                                                          ep::kWarps * 32, 0) == cudaSuccess;
+    d.epi_bwd_ctas = std::max(1, n);
     if (!fine) cudaGetLastError();
     d.ok = fine ? 1 : -1;
   });
@@ -237,12 +259,14 @@ int launch_status() {
 // ------------------------------------------------------------------------------------------
 namespace prof {
 enum Kind {
-  kQuant = 0, kDequant, kGemv, kGemvLoraDown, kTcGemm, kGemmFwd, kGemmBwd, kDropout, kKinds
+  kQuant = 0, kDequant, kGemv, kGemvLoraDown, kTcGemm, kGemmFwd, kGemmBwd, kDropout,
+  kEpilogueBwd, kNorm, kVocabGemm, kVocabRows, kKinds
 };
 const char* const kNames[kKinds] = {
     "nf4_quantize_kernel", "nf4_dequantize_kernel", "nf4_gemv_kernel",
     "gemv_lora_down_kernel", "tc_gemm_kernel",
-    "nf4_gemm_kernel<fwd>", "nf4_gemm_kernel<bwd>", "dropout_apply_kernel"};
+    "nf4_gemm_kernel<fwd>", "nf4_gemm_kernel<bwd>", "dropout_apply_kernel",
+    "epilogue_bwd_kernel", "norm_residual_kernels", "vocab_gemm_kernel", "vocab_row_kernels"};
 static_assert(kKinds == QLORA_KERNEL_KINDS, "kernel kinds");
 
 struct State {
@@ -508,13 +532,17 @@ LoraWs carve_lora(void* base, int64_t, int64_t) {
 
 // The fused NF4 GEMM runs as clusters of 2 CTAs (cta_group::2): grid x = 2 CTAs per 256-column
 // tile, grid y = 512-token row blocks.
-template <bool kBwd>
+template <bool kBwd, bool kEpi = false>
 int launch_nf4_gemm(const CUtensorMap& mA, const CUtensorMap& mP, const CUtensorMap& mA2,
                     const CUtensorMap& mB2, const Nf4GemmArgs& ga, int64_t t, int64_t ncols,
                     cudaStream_t st, int prof_kind) {
   // the output (t x ncols bf16) as 32-row x 64-column boxes for the epilogue's TMA stores
   CUtensorMap mOut;
   if (!map_bf16(&mOut, ga.out, static_cast<uint64_t>(ncols), static_cast<uint64_t>(t), 64, 32))
+    return QLORA_ERR_CUDA;
+  CUtensorMap mZ = mOut;   // a filler unless Z is kept
+  if (kEpi && ga.epi.z_out &&
+      !map_bf16(&mZ, ga.epi.z_out, static_cast<uint64_t>(ncols), static_cast<uint64_t>(t), 64, 32))
     return QLORA_ERR_CUDA;
   if ((t + tc::PAIR_M - 1) / tc::PAIR_M > 65535) return QLORA_ERR_BAD_SHAPE;  // grid y limit
   cudaLaunchConfig_t cfg = {};
@@ -537,7 +565,7 @@ int launch_nf4_gemm(const CUtensorMap& mA, const CUtensorMap& mP, const CUtensor
   cudaError_t e;
   {
     prof::Scope ps(prof_kind, st);
-    e = cudaLaunchKernelEx(&cfg, nf4_gemm_kernel<kBwd>, mA, mP, mA2, mB2, mOut, ga);
+    e = cudaLaunchKernelEx(&cfg, nf4_gemm_kernel<kBwd, kEpi>, mA, mP, mA2, mB2, mOut, mZ, ga);
   }
   if (e != cudaSuccess) {
     cudaGetLastError();
@@ -635,7 +663,7 @@ int check_bwd_args(const uint16_t* dY, const uint16_t* X, int64_t t, const nf4_w
 // dropout mask applied (s then carries the 1 / (1 - p)). Arguments already checked.
 int fwd_core(const uint16_t* X, const uint16_t* Xl, int64_t t, const nf4_weight* W,
              const uint16_t* L1, const uint16_t* L2, int64_t r, float s, uint16_t* Y,
-             uint16_t* sT_out, void* workspace, cudaStream_t st) {
+             uint16_t* sT_out, void* workspace, cudaStream_t st, const EpilogueArgs* epi = nullptr) {
   int dev, rc;
   if ((rc = current_device(&dev))) return rc;
   const int64_t h = W->in_features, o = W->out_features;
@@ -673,6 +701,7 @@ int fwd_core(const uint16_t* X, const uint16_t* Xl, int64_t t, const nf4_weight*
     ga.t = static_cast<int>(t);
     ga.r = static_cast<int>(r);
     ga.tab = device_table();
+    if (epi) ga.epi = *epi;
     // one CTA of 16 warps per SM (fewer when there are fewer units than warps, or capped)
     const int64_t units = (o / gv::kTileRows) * ((h / 64 + 1) / 2);
     int64_t ctas = std::min<int64_t>(sms, (units + gv::kWarps - 1) / gv::kWarps);
@@ -693,8 +722,9 @@ int fwd_core(const uint16_t* X, const uint16_t* Xl, int64_t t, const nf4_weight*
       attr[0].val.programmaticStreamSerializationAllowed = 1;
       cfg.attrs = attr;
       cfg.numAttrs = 1;
-      const cudaError_t e = t <= 8 ? cudaLaunchKernelEx(&cfg, nf4_gemv_kernel<1>, ga, mC)
-                                   : cudaLaunchKernelEx(&cfg, nf4_gemv_kernel<2>, ga, mC);
+      const auto kern = epi ? (t <= 8 ? nf4_gemv_kernel<1, true> : nf4_gemv_kernel<2, true>)
+                            : (t <= 8 ? nf4_gemv_kernel<1, false> : nf4_gemv_kernel<2, false>);
+      const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, ga, mC);
       if (e != cudaSuccess) return QLORA_ERR_CUDA;
     }
     return launch_status();
@@ -724,6 +754,10 @@ int fwd_core(const uint16_t* X, const uint16_t* Xl, int64_t t, const nf4_weight*
   ga.num_lkb = static_cast<int>((r + 63) / 64);
   ga.out = Y;
   ga.tab = device_table();
+  if (epi) {
+    ga.epi = *epi;
+    return launch_nf4_gemm<false, true>(mA, mP, mA2, mB2, ga, t, o, st, prof::kGemmFwd);
+  }
   return launch_nf4_gemm<false>(mA, mP, mA2, mB2, ga, t, o, st, prof::kGemmFwd);
 }
 
@@ -1023,6 +1057,7 @@ const char* qlora_status_string(int status) {
     case QLORA_ERR_UNSUPPORTED_DEVICE: return "QLORA_ERR_UNSUPPORTED_DEVICE: not an sm_100 GPU";
     case QLORA_ERR_SCRATCH_LIMIT:
       return "QLORA_ERR_SCRATCH_LIMIT: shape needs more than the static scratch holds";
+    case QLORA_DEV_TARGET: return "QLORA_DEV_TARGET: a target outside the vocabulary";
     case QLORA_DEV_NONFINITE: return "QLORA_DEV_NONFINITE: non-finite weight";
     case QLORA_DEV_TIMEOUT: return "QLORA_DEV_TIMEOUT: a kernel wait timed out";
     case QLORA_DEV_NONFINITE | QLORA_DEV_TIMEOUT:
@@ -1374,6 +1409,8 @@ extern "C" int qlora_linear_fwd_noalloc(const uint16_t* X, int64_t t, const nf4_
   return qlora_linear_fwd(X, t, W, L1, L2, r, s, Y, sT_out, scratch,
                           scratch ? static_cast<size_t>(QLORA_STATIC_SCRATCH_BYTES) : 0, stream);
 }
+
+#include "block_ops.cuh"
 
 #ifdef QLORA_TRACE
 extern "C" QLORA_API int qlora_trace_read(void* host, size_t bytes) {

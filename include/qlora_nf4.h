@@ -77,8 +77,9 @@ enum {
   QLORA_DEV_NONFINITE = 1,          /* nf4_quantize met a NaN or infinite weight             */
   QLORA_DEV_TIMEOUT = 2,            /* a kernel's bounded internal wait expired; outputs of
                                        that call are unspecified                              */
-  QLORA_DEV_LAUNCH = 4              /* a kernel found its launch unusable (e.g. too little
+  QLORA_DEV_LAUNCH = 4,             /* a kernel found its launch unusable (e.g. too little
                                        shared memory) and did no work                         */
+  QLORA_DEV_TARGET = 8              /* a vocabulary loss met a target outside the vocabulary  */
 };
 
 /* A packed NF4 weight: caller-owned device buffers plus the logical shape.
@@ -242,7 +243,7 @@ QLORA_API int qlora_get_last_status(qlora_stream_t stream);
  * or QLORA_ERR_INVALID_ARG if the profile overflowed its capacity. Kinds are numbered
  * 0 .. QLORA_KERNEL_KINDS-1 and named by qlora_kernel_name. Not thread-safe across
  * concurrent calls into the library while open. */
-#define QLORA_KERNEL_KINDS 8
+#define QLORA_KERNEL_KINDS 12
 QLORA_API int qlora_profile_begin(int capacity);
 QLORA_API int qlora_profile_end(double *ms, int64_t *launches, int nkinds);
 QLORA_API const char *qlora_kernel_name(int kind);
@@ -342,6 +343,91 @@ QLORA_API int qlora_adamw_step_multi(int ntensors, float *const *params, uint16_
                                      const int64_t *counts, float lr, float beta1, float beta2,
                                      float eps, float weight_decay, int64_t step, unsigned flags,
                                      qlora_stream_t stream);
+
+/* The linear with bias, activation and residual in its epilogue. There is no counterpart in the
+ * QLoRA method: it is what a block does with the linear's output next, without another pass:
+ *   Z = X.W' + s.X.L1.L2 + b,   Y = act(Z) + R,
+ * with Z held in fp32 and each output rounded once. The weight is frozen; b may be trained.
+ *   bias      device bf16, o values, or NULL.
+ *   act       QLORA_ACT_*: none; relu; gelu, z.Phi(z); gelu_tanh, its tanh form z.(1 + tanh(
+ *             sqrt(2/pi).(z + 0.044715 z^3)))/2; silu, z/(1 + exp(-z)).
+ *   residual  device bf16, t x o row-major, or NULL. It may be Y itself (updated in place); any
+ *             other overlap of an output with an input is not allowed.
+ *   Z_out     device bf16, t x o (output, bf16(Z), kept for qlora_epilogue_bwd) or NULL.
+ * Every other argument, the workspace (qlora_fwd_workspace_bytes) and the errors are those of
+ * qlora_linear_fwd; an unknown act gives INVALID_ARG. */
+#define QLORA_ACT_NONE 0
+#define QLORA_ACT_RELU 1
+#define QLORA_ACT_GELU 2
+#define QLORA_ACT_GELU_TANH 3
+#define QLORA_ACT_SILU 4
+QLORA_API int qlora_linear_fwd_epilogue(const uint16_t *X, int64_t t, const nf4_weight *W,
+                                        const uint16_t *L1, const uint16_t *L2, int64_t r, float s,
+                                        const uint16_t *bias, int act, const uint16_t *residual,
+                                        uint16_t *Y, uint16_t *Z_out, uint16_t *sT_out,
+                                        void *workspace, size_t ws_bytes, qlora_stream_t stream);
+
+/* qlora_epilogue_bwd -- the backward of that epilogue: dZ = dY . act'(Z) (elementwise) and
+ * db = sum over tokens of dZ. dZ then takes dY's place in qlora_linear_bwd; the residual's
+ * gradient is dY itself.
+ *   dY     device bf16, t x o.          Z: device bf16, t x o (the forward's Z_out), or NULL when
+ *          act is QLORA_ACT_NONE.       o % 8 == 0.
+ *   dZ     device bf16, t x o (output; may be dY itself) or NULL.
+ *   dbias  device fp32, o (output) or NULL. One of dZ and dbias is needed.
+ *   workspace, ws_bytes: at least qlora_epilogue_bwd_workspace_bytes(t, o) bytes when dbias is
+ *          given; not read otherwise.
+ * db sums the unrounded fp32 dZ, in an order fixed by t and o (results repeat bit for bit).
+ * relu'(0) = 0. Errors: INVALID_ARG, BAD_SHAPE, MISALIGNED, WORKSPACE, CUDA. */
+QLORA_API int qlora_epilogue_bwd(const uint16_t *dY, const uint16_t *Z, int64_t t, int64_t o, int act,
+                                 uint16_t *dZ, float *dbias, void *workspace, size_t ws_bytes,
+                                 qlora_stream_t stream);
+QLORA_API size_t qlora_epilogue_bwd_workspace_bytes(int64_t t, int64_t o);
+
+/* qlora_norm_residual_fwd -- the norms before and after a block, fused with the block's gate and
+ * its residual scale: what stands between the last linear of one block and the first of the next.
+ * No counterpart in the QLoRA method. With rstd(a) = 1 / sqrt(mean(a^2) + eps) over a token's h values:
+ *   u  = y . rstd(y) . w_post      (u = y without w_post)
+ *   x' = x + scale . gate . u      (x' = x without y)
+ *   n  = x' . rstd(x') . w_pre
+ * in fp32, x' and n each rounded once to bf16 (n is formed from the unrounded x').
+ *   x, y     device bf16, t x h row-major; y may be NULL (then w_post and gate must be).
+ *            8 <= h <= 16384, h % 8 == 0.
+ *   w_post, w_pre  device bf16, h, or NULL (no such norm).
+ *   gate     device bf16, ceil(t / rows_per_gate) x h: token i takes row i / rows_per_gate (1: a
+ *            gate per token; the tokens of a sequence: a gate per sequence; >= t: one for all);
+ *            or NULL (rows_per_gate is then ignored).
+ *   x_out    device bf16, t x h (output); may be x itself; may be NULL when only n is wanted.
+ *   n_out    device bf16, t x h (output), given exactly when w_pre is.
+ *   rstd_post, rstd_pre  device fp32, t each (outputs for the backward, 4-byte aligned) or NULL.
+ * Errors: INVALID_ARG (NULL combinations, eps < 0 or not finite, rows_per_gate < 1), BAD_SHAPE,
+ * MISALIGNED, CUDA. */
+QLORA_API int qlora_norm_residual_fwd(const uint16_t *x, const uint16_t *y, int64_t t, int64_t h,
+                                      const uint16_t *w_post, const uint16_t *gate, int64_t rows_per_gate,
+                                      float scale, const uint16_t *w_pre, float eps, uint16_t *x_out,
+                                      uint16_t *n_out, float *rstd_post, float *rstd_pre,
+                                      qlora_stream_t stream);
+
+/* qlora_norm_residual_bwd -- its gradients.
+ *   dx_out   device bf16, t x h: gradient of x', or NULL (zero).
+ *   dn       device bf16, t x h: gradient of n; given exactly when w_pre is, with x_out (the
+ *            forward's x') and rstd_pre (the forward's).
+ *   y, w_post, gate, rows_per_gate, scale, w_pre: the forward's; rstd_post: the forward's, given
+ *            exactly when w_post is.
+ *   dx       device bf16, t x h (output): gradient of x.
+ *   dy       device bf16, t x h (output), given exactly when y is.
+ *   dw_post (h), dgate (ceil(t / rows_per_gate) x h), dw_pre (h)  device fp32 (outputs), given
+ *            exactly when w_post, gate, w_pre are.
+ *   workspace, ws_bytes: at least qlora_norm_residual_bwd_workspace_bytes(t, h) bytes.
+ * The sums over tokens are taken in an order fixed by t, h and rows_per_gate (no atomics).
+ * Errors: as the forward, and WORKSPACE. */
+QLORA_API int qlora_norm_residual_bwd(const uint16_t *dx_out, const uint16_t *dn, const uint16_t *x_out,
+                                      const uint16_t *y, int64_t t, int64_t h, const uint16_t *w_post,
+                                      const uint16_t *gate, int64_t rows_per_gate, float scale,
+                                      const uint16_t *w_pre, const float *rstd_post, const float *rstd_pre,
+                                      uint16_t *dx, uint16_t *dy, float *dw_post, float *dgate,
+                                      float *dw_pre, void *workspace, size_t ws_bytes,
+                                      qlora_stream_t stream);
+QLORA_API size_t qlora_norm_residual_bwd_workspace_bytes(int64_t t, int64_t h);
 
 /* Launch shape of the decode GEMV (t <= 16), a scheduling knob with no counterpart in the
  * method. By default the GEMV runs one CTA of 16 warps per SM and splits its units (32 rows x
