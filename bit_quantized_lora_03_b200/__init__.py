@@ -6,4 +6,5 @@ The compute lives in the C-ABI library libqlora_nf4.so (hand-written CUDA kernel
 
 from .binding import (PackedNF4, codebook, last_status, nf4_dequantize, nf4_quantize,  # noqa: F401
                       qlora_epilogue_bwd, qlora_linear_bwd, qlora_linear_fwd,
-                      qlora_linear_fwd_epilogue, qlora_norm_residual_bwd, qlora_norm_residual_fwd)
+                      qlora_linear_fwd_epilogue, qlora_norm_residual_bwd, qlora_norm_residual_fwd,
+                      qlora_vocab_loss_bwd, qlora_vocab_loss_fwd, qlora_vocab_loss_fwd_bwd)

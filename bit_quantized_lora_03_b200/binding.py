@@ -90,6 +90,15 @@ SIGNATURES = {
                                                ctypes.c_float, _PTR, _PTR, _PTR, _PTR, _PTR, _PTR,
                                                _PTR, _PTR, _PTR, ctypes.c_size_t, _PTR]),
     "qlora_norm_residual_bwd_workspace_bytes": (ctypes.c_size_t, [_I64, _I64]),
+    "qlora_vocab_loss_fwd": (ctypes.c_int, [_PTR, _PTR, _I64, _I64, _I64, _PTR, _I64, _PTR, _PTR, _PTR,
+                                            ctypes.c_size_t, _PTR]),
+    "qlora_vocab_loss_bwd": (ctypes.c_int, [_PTR, _PTR, _I64, _I64, _I64, _PTR, _I64, _PTR, _PTR, _PTR,
+                                            _PTR, _PTR, ctypes.c_size_t, _PTR]),
+    "qlora_vocab_loss_fwd_bwd": (ctypes.c_int, [_PTR, _PTR, _I64, _I64, _I64, _PTR, _I64, _PTR, _PTR,
+                                                _PTR, _PTR, _PTR, ctypes.c_size_t, _PTR]),
+    "qlora_vocab_loss_fwd_workspace_bytes": (ctypes.c_size_t, [_I64, _I64, _I64]),
+    "qlora_vocab_loss_bwd_workspace_bytes": (ctypes.c_size_t, [_I64, _I64, _I64]),
+    "qlora_vocab_loss_fwd_bwd_workspace_bytes": (ctypes.c_size_t, [_I64, _I64, _I64]),
 }
 KERNEL_KINDS = 12
 
@@ -584,6 +593,63 @@ def qlora_norm_residual_bwd(dx_out: torch.Tensor | None, dn: torch.Tensor | None
         if dn is None and w_pre is not None:
             dwi = torch.zeros(h, dtype=f32, device=dev)
     return dx, dy, dwo, dg, dwi
+
+
+def _vocab(X, W, targets):
+    """(t, h, v) and the addresses of the loss's inputs, checked."""
+    (t, h), (v, _), dev = _matrix(X, "X"), _matrix(W, "W"), X.device
+    return (t, h, v), (_on(dev, X, torch.bfloat16, (t, h), "X"), _on(dev, W, torch.bfloat16, (v, h), "W"), t, h, v,
+                       _on(dev, targets, torch.int64, (t,), "targets"))
+
+
+def qlora_vocab_loss_fwd(X: torch.Tensor, W: torch.Tensor, targets: torch.Tensor, ignore_index: int = -100,
+                         loss: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                         ws: torch.Tensor | None = None, stream=None):
+    """Cross entropy of X.W^T (t x v, never stored) against int64 targets: (loss t fp32, lse t fp32).
+    Targets equal to ignore_index are not counted (loss 0)."""
+    with _guard(X, stream):
+        (t, h, v), args = _vocab(X, W, targets)
+        dev, f32 = X.device, torch.float32
+        loss, lse = _out(dev, loss, f32, (t,), "loss"), _out(dev, lse, f32, (t,), "lse")
+        ws = _scratch(dev, ws, int(lib().qlora_vocab_loss_fwd_workspace_bytes(t, h, v)))
+        _check(lib().qlora_vocab_loss_fwd(*args, int(ignore_index), loss.data_ptr(), lse.data_ptr(),
+                                          ws.data_ptr(), ws.numel(), _stream()), "qlora_vocab_loss_fwd")
+    return loss, lse
+
+
+def qlora_vocab_loss_bwd(X: torch.Tensor, W: torch.Tensor, targets: torch.Tensor, lse: torch.Tensor,
+                         dloss: torch.Tensor, dlse: torch.Tensor | None = None, ignore_index: int = -100,
+                         dX: torch.Tensor | None = None, ws: torch.Tensor | None = None, stream=None):
+    """dX (t x h bf16) from the gradients of loss (and of lse, if given; t fp32 each) and the
+    forward's lse; W is frozen."""
+    with _guard(X, stream):
+        (t, h, v), args = _vocab(X, W, targets)
+        dev, f32 = X.device, torch.float32
+        grads = (_on(dev, lse, f32, (t,), "lse"), _on(dev, dloss, f32, (t,), "dloss"), _on(dev, dlse, f32, (t,), "dlse"))
+        dX = _out(dev, dX, torch.bfloat16, (t, h), "dX")
+        ws = _scratch(dev, ws, int(lib().qlora_vocab_loss_bwd_workspace_bytes(t, h, v)))
+        _check(lib().qlora_vocab_loss_bwd(*args, int(ignore_index), *grads, dX.data_ptr(), ws.data_ptr(),
+                                          ws.numel(), _stream()), "qlora_vocab_loss_bwd")
+    return dX
+
+
+def qlora_vocab_loss_fwd_bwd(X: torch.Tensor, W: torch.Tensor, targets: torch.Tensor, dloss: torch.Tensor,
+                             ignore_index: int = -100, loss: torch.Tensor | None = None,
+                             lse: torch.Tensor | None = None, dX: torch.Tensor | None = None,
+                             ws: torch.Tensor | None = None, stream=None):
+    """(loss, lse, dX) in one call for a dloss (t fp32) known beforehand, such as 1 / count for the
+    mean: the logits are formed once."""
+    with _guard(X, stream):
+        (t, h, v), args = _vocab(X, W, targets)
+        dev, f32 = X.device, torch.float32
+        d = _on(dev, dloss, f32, (t,), "dloss")
+        loss, lse = _out(dev, loss, f32, (t,), "loss"), _out(dev, lse, f32, (t,), "lse")
+        dX = _out(dev, dX, torch.bfloat16, (t, h), "dX")
+        ws = _scratch(dev, ws, int(lib().qlora_vocab_loss_fwd_bwd_workspace_bytes(t, h, v)))
+        _check(lib().qlora_vocab_loss_fwd_bwd(*args, int(ignore_index), d, loss.data_ptr(), lse.data_ptr(),
+                                              dX.data_ptr(), ws.data_ptr(), ws.numel(), _stream()),
+               "qlora_vocab_loss_fwd_bwd")
+    return loss, lse, dX
 
 
 class KernelProfile:

@@ -1,5 +1,5 @@
 // Host side of the operators around the linear: the fused epilogue, the norms of a block with its
-// gate and residual scale. Included by qlora_nf4.cu, whose argument checks, device table and launch
+// gate and residual scale, the vocabulary loss. Included by qlora_nf4.cu, whose argument checks, device table and launch
 // helpers it uses.
 #pragma once
 
@@ -71,6 +71,204 @@ NormBwdPlan plan_norm_bwd(int64_t t, int64_t h, int sms) {
 }
 
 constexpr int kMaxSms = 160;   // workspace sizes are host functions: sized for any B200
+
+// ------------------------------------------------------------------------------------------
+// vocabulary loss
+// ------------------------------------------------------------------------------------------
+// Tokens whose g (or scaled exponentials) the workspace holds at a time: as many as fit 256 MiB,
+// at least one row of tiles. Few long runs keep the second product's tiles busy and read W seldom.
+constexpr size_t kVocabRunBytes = size_t(256) << 20;
+constexpr int64_t kVocabMaxV = int64_t(1) << 24;
+constexpr int kVocabMaxParts = kMaxSms;   // partial tiles of a split K
+
+struct VocabPlan {
+  int64_t run;      // tokens per run
+  int64_t ldp;      // v rounded up to 64
+  int64_t n_tiles;  // pieces of the vocabulary
+  size_t g_bytes, stats_bytes, target_bytes, part_bytes;
+};
+VocabPlan plan_vocab(int64_t t, int64_t v, bool stats, bool grad) {
+  VocabPlan p{};
+  p.ldp = (v + 63) / 64 * 64;
+  p.n_tiles = (v + vg::BN - 1) / vg::BN;
+  const int64_t fit = static_cast<int64_t>(kVocabRunBytes / (static_cast<size_t>(p.ldp) * 2));
+  p.run = grad ? std::min<int64_t>(t, std::max<int64_t>(vg::BM, fit / vg::BM * vg::BM)) : t;
+  if (grad) {
+    p.g_bytes = align256(static_cast<size_t>(p.run) * p.ldp * 2);
+    p.part_bytes = static_cast<size_t>(kVocabMaxParts) * vg::BM * vg::BN * 4;
+  }
+  if (stats) {
+    p.stats_bytes = align256(static_cast<size_t>(p.run) * p.n_tiles * 8);
+    p.target_bytes = align256(static_cast<size_t>(p.run) * 4);
+  }
+  return p;
+}
+
+int check_vocab_shape(int64_t t, int64_t h, int64_t v) {
+  if (t < 1 || v < 1) return QLORA_ERR_INVALID_ARG;
+  if (h < 8 || h % 8 != 0 || h >= kMaxDim || t >= kMaxDim || v > kVocabMaxV) return QLORA_ERR_BAD_SHAPE;
+  return QLORA_OK;
+}
+
+size_t vocab_ws_bytes(int64_t t, int64_t h, int64_t v, bool stats, bool grad) {
+  if (check_vocab_shape(t, h, v) != QLORA_OK) return 0;
+  const VocabPlan p = plan_vocab(t, v, stats, grad);
+  return p.g_bytes + p.stats_bytes + p.target_bytes + p.part_bytes;
+}
+
+// Tiles, their order and their split. Pairs walk the list in steps; row tiles are walked in groups
+// of 16 (4096 tokens) per column tile, so that a group's A and the column tiles in flight stay in L2.
+// The tiles of the last, partly filled round are split along K (fp32 partial tiles, joined in order)
+// into the number of pieces that ends the round soonest.
+VocabGemmArgs plan_vocab_gemm(int64_t M, int64_t N, int64_t K, bool split, int pairs) {
+  VocabGemmArgs a{};
+  a.M = static_cast<int>(M);
+  a.N = static_cast<int>(N);
+  a.num_kb = static_cast<int>((K + vg::BK - 1) / vg::BK);
+  a.m_tiles = static_cast<int>((M + vg::BM - 1) / vg::BM);
+  a.n_tiles = static_cast<int>((N + vg::BN - 1) / vg::BN);
+  a.m_group = std::min(a.m_tiles, 16);
+  const int64_t tiles = static_cast<int64_t>(a.m_tiles) * a.n_tiles;
+  const int rest = static_cast<int>(tiles % pairs);
+  a.splits = 1;
+  double best = 1.0;
+  for (int s = 2; split && rest && rest * s <= kVocabMaxParts && s <= a.num_kb / 4; ++s) {
+    const double cost = static_cast<double>((rest * s + pairs - 1) / pairs) / s + 0.01 * s;
+    if (cost < best) {
+      best = cost;
+      a.splits = s;
+    }
+  }
+  a.kb_per_split = (a.num_kb + a.splits - 1) / a.splits;
+  a.splits = (a.num_kb + a.kb_per_split - 1) / a.kb_per_split;   // no empty piece
+  a.whole = static_cast<int>(a.splits > 1 ? tiles - rest : tiles);
+  a.items = static_cast<int>(a.whole + (tiles - a.whole) * a.splits);
+  return a;
+}
+
+template <int kMode>
+int launch_vocab_gemm(const CUtensorMap& mA, const CUtensorMap& mB, const CUtensorMap& mOut,
+                      const CUtensorMap& mPart, const VocabGemmArgs& a, int pairs, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min(pairs, a.items)), 1, 1);
+  cfg.blockDim = dim3(vg::kThreads, 1, 1);
+  cfg.dynamicSmemBytes = vg::smem_bytes();
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t e;
+  {
+    prof::Scope ps(prof::kVocabGemm, st);
+    e = cudaLaunchKernelEx(&cfg, vocab_gemm_kernel<kMode>, mA, mB, mOut, mPart, a);
+  }
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return QLORA_ERR_CUDA;
+  }
+  return launch_status();
+}
+
+struct VocabCall {
+  const uint16_t *X, *W;
+  int64_t t, h, v;
+  const int64_t* targets;
+  int64_t ignore;
+  float *loss, *lse;        // outputs (lse an input of the backward alone)
+  const float *dloss, *dlse;
+  uint16_t* dX;
+};
+
+// The loss (dX == NULL), the loss and its gradient (loss and dX), or the gradient alone.
+int vocab_core(const VocabCall& c, void* workspace, cudaStream_t st) {
+  int dev, rc;
+  if ((rc = current_device(&dev))) return rc;
+  if (sm_count(dev) > kMaxSms) return QLORA_ERR_UNSUPPORTED_DEVICE;
+  const int pairs = sm_count(dev) / 2;
+  const bool stats = c.loss != nullptr, grad = c.dX != nullptr;
+  const VocabPlan p = plan_vocab(c.t, c.v, stats, grad);
+  uint8_t* ws = reinterpret_cast<uint8_t*>(workspace);
+  uint16_t* g = reinterpret_cast<uint16_t*>(ws);
+  float* part = reinterpret_cast<float*>(ws + p.g_bytes);
+  float2* st2 = reinterpret_cast<float2*>(ws + p.g_bytes + p.part_bytes);
+  float* tl = reinterpret_cast<float*>(ws + p.g_bytes + p.part_bytes + p.stats_bytes);
+  CUtensorMap mWk, mWmn, mPart;
+  if (!map_bf16(&mWk, c.W, c.h, c.v, 64, 128) || !map_bf16(&mWmn, c.W, c.h, c.v, 64, 64)) return QLORA_ERR_CUDA;
+  if (grad && !make_map_2d(&mPart, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, part, vg::BN, kVocabMaxParts * vg::BM,
+                           vg::BN * 4, 32, 32, true))
+    return QLORA_ERR_CUDA;
+  for (int64_t i0 = 0; i0 < c.t; i0 += p.run) {
+    const int64_t n = std::min(p.run, c.t - i0);
+    CUtensorMap mX, mG, mGs, mD;
+    if (!map_bf16(&mX, c.X + i0 * c.h, c.h, n, 64, 128)) return QLORA_ERR_CUDA;
+    if (grad && (!map_bf16(&mG, g, p.ldp, n, 64, 128) || !map_bf16(&mGs, g, p.ldp, n, 64, 32) ||
+                 !map_bf16(&mD, c.dX + i0 * c.h, c.h, n, 64, 32)))
+      return QLORA_ERR_CUDA;
+    VocabGemmArgs a = plan_vocab_gemm(n, c.v, c.h, false, pairs);
+    a.ldp = static_cast<int>(p.ldp);
+    a.targets = c.targets + i0;
+    a.ignore = c.ignore;
+    a.stats = st2;
+    a.target_logit = tl;
+    if (stats) {
+      rc = grad ? launch_vocab_gemm<kVocabScaled>(mX, mWk, mGs, mX, a, pairs, st)
+                : launch_vocab_gemm<kVocabStats>(mX, mWk, mX, mX, a, pairs, st);
+      if (rc) return rc;
+      VocabRowArgs r{};
+      r.stats = st2;
+      r.target_logit = tl;
+      r.targets = a.targets;
+      r.ignore = c.ignore;
+      r.t = static_cast<int>(n);
+      r.v = static_cast<int>(c.v);
+      r.n_tiles = a.n_tiles;
+      r.loss = c.loss + i0;
+      r.lse = c.lse + i0;
+      {
+        prof::Scope ps(prof::kVocabRows, st);
+        if (grad) {
+          r.dloss = c.dloss + i0;
+          r.g = g;
+          r.ldp = a.ldp;
+          vocab_scale_kernel<<<static_cast<unsigned>(n), 256, 0, st>>>(r);
+        } else {
+          vocab_rows_kernel<<<static_cast<unsigned>((n + 7) / 8), 256, 0, st>>>(r);
+        }
+      }
+      if ((rc = launch_status())) return rc;
+    } else {
+      a.lse = c.lse + i0;
+      a.dloss = c.dloss + i0;
+      a.dlse = c.dlse ? c.dlse + i0 : nullptr;
+      if ((rc = launch_vocab_gemm<kVocabProb>(mX, mWk, mGs, mX, a, pairs, st))) return rc;
+    }
+    if (!grad) continue;
+    const VocabGemmArgs d = plan_vocab_gemm(n, c.h, c.v, true, pairs);
+    if ((rc = launch_vocab_gemm<kVocabGrad>(mG, mWmn, mD, mPart, d, pairs, st))) return rc;
+    if (d.splits > 1) {
+      const int tiles = d.m_tiles * d.n_tiles - d.whole;
+      vocab_join_kernel<<<dim3(static_cast<unsigned>(tiles), vg::BM / 8), 256, 0, st>>>(part, c.dX + i0 * c.h, d);
+      if ((rc = launch_status())) return rc;
+    }
+  }
+  return QLORA_OK;
+}
+
+int check_vocab_args(const VocabCall& c, bool stats, bool grad, const void* workspace) {
+  if (!c.X || !c.W || !c.targets || !c.lse || (stats && !c.loss) || (grad && (!c.dX || !c.dloss)))
+    return QLORA_ERR_INVALID_ARG;
+  int rc = check_vocab_shape(c.t, c.h, c.v);
+  if (rc) return rc;
+  if (!aligned16(c.X) || !aligned16(c.W) || (c.dX && !aligned16(c.dX)) || (workspace && !aligned16(workspace)) ||
+      (reinterpret_cast<uintptr_t>(c.targets) & 7u) || !aligned4(c.loss) || !aligned4(c.lse) ||
+      !aligned4(c.dloss) || !aligned4(c.dlse))
+    return QLORA_ERR_MISALIGNED;
+  return QLORA_OK;
+}
 
 }  // namespace
 
@@ -275,6 +473,47 @@ int qlora_norm_residual_bwd(const uint16_t* dx_out, const uint16_t* dn, const ui
                     pl.units, 2 + gate_blocks, st) != cudaSuccess)
     return QLORA_ERR_CUDA;
   return QLORA_OK;
+}
+
+size_t qlora_vocab_loss_fwd_workspace_bytes(int64_t t, int64_t h, int64_t v) {
+  return vocab_ws_bytes(t, h, v, true, false);
+}
+size_t qlora_vocab_loss_bwd_workspace_bytes(int64_t t, int64_t h, int64_t v) {
+  return vocab_ws_bytes(t, h, v, false, true);
+}
+size_t qlora_vocab_loss_fwd_bwd_workspace_bytes(int64_t t, int64_t h, int64_t v) {
+  return vocab_ws_bytes(t, h, v, true, true);
+}
+
+int qlora_vocab_loss_fwd(const uint16_t* X, const uint16_t* W, int64_t t, int64_t h, int64_t v,
+                         const int64_t* targets, int64_t ignore_index, float* loss, float* lse, void* workspace,
+                         size_t ws_bytes, qlora_stream_t stream) {
+  const VocabCall c{X, W, t, h, v, targets, ignore_index, loss, lse, nullptr, nullptr, nullptr};
+  const int rc = check_vocab_args(c, true, false, workspace);
+  if (rc) return rc;
+  if (!workspace || ws_bytes < qlora_vocab_loss_fwd_workspace_bytes(t, h, v)) return QLORA_ERR_WORKSPACE;
+  return vocab_core(c, workspace, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int qlora_vocab_loss_bwd(const uint16_t* X, const uint16_t* W, int64_t t, int64_t h, int64_t v,
+                         const int64_t* targets, int64_t ignore_index, const float* lse, const float* dloss,
+                         const float* dlse, uint16_t* dX, void* workspace, size_t ws_bytes,
+                         qlora_stream_t stream) {
+  const VocabCall c{X, W, t, h, v, targets, ignore_index, nullptr, const_cast<float*>(lse), dloss, dlse, dX};
+  const int rc = check_vocab_args(c, false, true, workspace);
+  if (rc) return rc;
+  if (!workspace || ws_bytes < qlora_vocab_loss_bwd_workspace_bytes(t, h, v)) return QLORA_ERR_WORKSPACE;
+  return vocab_core(c, workspace, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int qlora_vocab_loss_fwd_bwd(const uint16_t* X, const uint16_t* W, int64_t t, int64_t h, int64_t v,
+                             const int64_t* targets, int64_t ignore_index, const float* dloss, float* loss,
+                             float* lse, uint16_t* dX, void* workspace, size_t ws_bytes, qlora_stream_t stream) {
+  const VocabCall c{X, W, t, h, v, targets, ignore_index, loss, lse, dloss, nullptr, dX};
+  const int rc = check_vocab_args(c, true, true, workspace);
+  if (rc) return rc;
+  if (!workspace || ws_bytes < qlora_vocab_loss_fwd_bwd_workspace_bytes(t, h, v)) return QLORA_ERR_WORKSPACE;
+  return vocab_core(c, workspace, reinterpret_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

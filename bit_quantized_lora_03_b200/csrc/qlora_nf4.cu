@@ -23,6 +23,7 @@
 #include "nf4_gemv.cuh"
 #include "norm_residual.cuh"
 #include "epilogue.cuh"
+#include "vocab_loss.cuh"
 
 using namespace qlora;
 
@@ -150,6 +151,10 @@ bool block_ops_attributes() {
   bool fine = true;
   fine &= cudaFuncSetAttribute(norm_residual_bwd_kernel<2, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                nr::kMaxH * 3 * 4) == cudaSuccess;
+  for (auto* kernel : {vocab_gemm_kernel<kVocabStats>, vocab_gemm_kernel<kVocabScaled>,
+                       vocab_gemm_kernel<kVocabProb>, vocab_gemm_kernel<kVocabGrad>})
+    fine &= cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 static_cast<int>(vg::smem_bytes())) == cudaSuccess;
   return fine;
 }
 

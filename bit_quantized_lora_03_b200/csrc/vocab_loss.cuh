@@ -1,0 +1,509 @@
+// Softmax cross entropy through a frozen output head, and its gradient, without a t x v matrix of
+// logits: l = X.W^T (X t x h hidden states, W v x h head, both bf16),
+//   lse_i = log sum_v exp(l_iv),  loss_i = lse_i - l_i[y_i]  (0 where y_i is not counted),
+//   dX_i  = sum_v g_iv W_v,  g_iv = a_i p_iv - b_i [v = y_i],  p_iv = exp(l_iv - lse_i),
+//   b_i   = dloss_i (0 where y_i is not counted),  a_i = b_i + dlse_i.
+//
+// vocab_gemm_kernel is one persistent tcgen05 GEMM with four epilogues. The vocabulary is walked in
+// pieces of 256 columns: a CTA pair computes 256 tokens x 256 columns of logits into tensor memory
+// (fp32) and its epilogue reduces them there:
+//   kVocabStats   a token's maximum and sum of exponentials over the piece (and the target's logit)
+//   kVocabScaled  the same, and exp(l - the piece's maximum) in bf16, for the one-call form
+//   kVocabProb    g in bf16, lse being known
+//   kVocabGrad    (the second product, dX = g.W) dX in bf16, or fp32 partial tiles of a split K
+// Only statistics leave the first kernel: 8 bytes per token and piece instead of 512. The backward
+// holds g (or the scaled exponentials) of a bounded run of tokens at a time in the workspace.
+//
+// Bound: the tensor cores (2thv per product) for more than a few hundred tokens, reading W for few.
+// The design follows from the first: cta_group::2 (256 x 256 x 16 per instruction, each CTA loading
+// half of A and half of B), a six-stage TMA ring, and two accumulators in tensor memory, so that a
+// tile's epilogue (four warps) runs under the next tile's products. g is rounded to bf16 because it
+// is an operand of a bf16 product: a relative 2^-9 per term, against the 2^-9 of dX's own rounding.
+//
+// Every wait is bounded (qlora::mbar_wait); on expiry the CTA reports QLORA_DEV_TIMEOUT, stops
+// issuing, waits for its own copies and MMAs in flight, frees TMEM and returns.
+#pragma once
+
+#include "nf4_gemm.cuh"
+
+namespace qlora {
+
+namespace vg {
+constexpr int BM = 256, BN = 256, BK = 64;   // per CTA pair
+constexpr int STAGES = 6;
+constexpr int A_BYTES = 128 * BK * 2;        // this CTA's half of A
+constexpr int B_BYTES = 128 * BK * 2;        // and of B
+constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+constexpr int kEpiWarps = 4;
+constexpr int kTmaWarp = 4, kMmaWarp = 5;
+constexpr int kThreads = 6 * 32;
+constexpr int kStaging = kEpiWarps * 2 * 4096;   // two 32-row x 128-byte tiles per epilogue warp
+constexpr int kTmemCols = 512;
+constexpr size_t smem_bytes() { return 1024 + STAGES * STAGE_BYTES + kStaging + 256; }
+static_assert(smem_bytes() <= 232448, "fits the opt-in shared memory of one CTA");
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+}  // namespace vg
+
+enum VocabMode : int { kVocabStats = 0, kVocabScaled = 1, kVocabProb = 2, kVocabGrad = 3 };
+
+struct VocabGemmArgs {
+  int M, N;              // rows and columns of the product (N: v, or h for kVocabGrad)
+  int num_kb;            // K-steps of 64
+  int m_tiles, n_tiles;
+  int m_group;           // row tiles that are walked together, column tile by column tile
+  int whole;             // tiles computed in one piece; the ones behind are split along K
+  int splits, kb_per_split;
+  int items;             // whole + (tiles - whole) * splits
+  int ldp;               // columns of the stored g (v rounded up to 64)
+  const int64_t* targets;
+  int64_t ignore;
+  float2* stats;         // M x n_tiles: (maximum, sum of exp(l - maximum))
+  float* target_logit;   // M
+  const float* lse;      // kVocabProb
+  const float* dloss;
+  const float* dlse;     // or NULL
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t tmem_ld_1(uint32_t taddr) {
+  uint32_t v;
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(v) : "r"(taddr));
+  return v;
+}
+
+struct VocabItem {
+  int m0, n0, nt, kb0, kb1, part;   // part: the partial tile's index, or -1
+};
+__device__ __forceinline__ VocabItem vocab_item(const VocabGemmArgs& a, int item) {
+  VocabItem it;
+  int tile = item;
+  it.kb0 = 0;
+  it.kb1 = a.num_kb;
+  it.part = -1;
+  if (item >= a.whole) {
+    const int j = item - a.whole, sp = j % a.splits;
+    tile = a.whole + j / a.splits;
+    it.kb0 = sp * a.kb_per_split;
+    it.kb1 = min(a.num_kb, it.kb0 + a.kb_per_split);
+    if (a.splits > 1) it.part = j;
+  }
+  const int per = a.m_group * a.n_tiles, g = tile / per, rem = tile - g * per;
+  const int gm = min(a.m_group, a.m_tiles - g * a.m_group);
+  it.nt = rem / gm;
+  it.m0 = (g * a.m_group + rem - it.nt * gm) * vg::BM;
+  it.n0 = it.nt * vg::BN;
+  return it;
+}
+
+template <int kMode>
+__global__ void __launch_bounds__(vg::kThreads, 1)
+    vocab_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                      const __grid_constant__ CUtensorMap tmOut, const __grid_constant__ CUtensorMap tmPart,
+                      const VocabGemmArgs args) {
+  using namespace vg;
+  constexpr bool kBmn = kMode == kVocabGrad;   // W as the K-major operand (logits) or the MN-major one
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint8_t* staging = smem + STAGES * STAGE_BYTES;
+  uint64_t* full = reinterpret_cast<uint64_t*>(staging + kStaging);
+  uint64_t* empty = full + STAGES;
+  uint64_t* peer_ready = empty + STAGES;   // even CTA: the odd CTA's stage has landed
+  uint64_t* acc_full = peer_ready + STAGES;
+  uint64_t* acc_empty = acc_full + 2;      // even CTA: both CTAs have drained the accumulator
+  uint64_t* drained = acc_empty + 2;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drained + 1);
+  volatile uint32_t* abort_flag = tmem_holder + 1;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_ctarank());   // 0: MMA issuer, 1: its peer
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+      mbar_init(&peer_ready[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&acc_full[b], 1);
+      mbar_init(&acc_empty[b], 2 * kEpiWarps);
+    }
+    mbar_init(drained, 1);
+    *abort_flag = 0u;
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc2(tmem_holder, kTmemCols);
+    tmem_relinquish2();
+  }
+  if (warp == kTmaWarp && lane == 0) {
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmB);
+    tma_prefetch_desc(&tmOut);
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();   // both CTAs' barriers exist before any cross-CTA arrive
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_holder;
+
+  if (warp == kTmaWarp) {
+    if (lane == 0) {
+      int g = 0;
+      bool ok = true;
+      for (int item = pair; ok && item < args.items; item += pairs) {
+        const VocabItem it = vocab_item(args, item);
+        for (int kb = it.kb0; kb < it.kb1; ++kb, ++g) {
+          const int slot = g % STAGES;
+          if (!mbar_wait(&empty[slot], ((g / STAGES) & 1) ^ 1u, abort_flag)) { ok = false; break; }
+          uint8_t* dst = smem + slot * STAGE_BYTES;
+          mbar_arrive_expect_tx(&full[slot], STAGE_BYTES);
+          tma_load_2d(dst, &tmA, &full[slot], kb * BK, it.m0 + rank * 128);
+          if (!kBmn) {
+            tma_load_2d(dst + A_BYTES, &tmB, &full[slot], kb * BK, it.n0 + rank * 128);
+          } else {
+            tma_load_2d(dst + A_BYTES, &tmB, &full[slot], it.n0 + rank * 128, kb * BK);
+            tma_load_2d(dst + A_BYTES + 8192, &tmB, &full[slot], it.n0 + rank * 128 + 64, kb * BK);
+          }
+        }
+      }
+      if (*abort_flag)   // no copy may still be writing this CTA's shared memory when it exits
+        for (int j = (g > STAGES ? g - STAGES : 0); j < g; ++j) mbar_drain(&full[j % STAGES], (j / STAGES) & 1);
+    }
+  } else if (warp == kMmaWarp) {
+    if (lane == 0 && rank == 0) {
+      constexpr uint32_t kIdesc = idesc_bf16(BM, BN, false, kBmn);
+      int g = 0, n = 0;
+      bool ok = true;
+      for (int item = pair; ok && item < args.items; item += pairs, ++n) {
+        const VocabItem it = vocab_item(args, item);
+        const int buf = n & 1;
+        if (!mbar_wait_cluster(&acc_empty[buf], ((n >> 1) & 1) ^ 1u, abort_flag)) break;
+        tc_fence_after();
+        for (int kb = it.kb0; kb < it.kb1; ++kb, ++g) {
+          const int slot = g % STAGES;
+          const uint32_t ph = (g / STAGES) & 1;
+          if (!mbar_wait(&full[slot], ph, abort_flag) || !mbar_wait_cluster(&peer_ready[slot], ph, abort_flag)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a_addr = smem_addr(smem + slot * STAGE_BYTES), b_addr = a_addr + A_BYTES;
+#pragma unroll
+          for (int kk = 0; kk < BK / 16; ++kk) {
+            const uint64_t ad = sw128_desc(a_addr + kk * 32, 16, 1024);
+            const uint64_t bd = kBmn ? sw128_desc(b_addr + kk * 2048, 8192, 1024)
+                                     : sw128_desc(b_addr + kk * 32, 16, 1024);
+            umma2_bf16(tmem_base + buf * BN, ad, bd, kIdesc, (kb > it.kb0 || kk > 0) ? 1u : 0u);
+          }
+          umma2_commit_multicast(&empty[slot], 0x3);   // frees the stage in both CTAs
+        }
+        umma2_commit_multicast(&acc_full[buf], 0x3);
+      }
+      umma2_commit_multicast(drained, 0x1);   // every MMA has read its operands before the CTAs leave
+      mbar_drain(drained, 0);
+    } else if (lane == 0) {
+      int g = 0;
+      bool ok = true;
+      for (int item = pair; ok && item < args.items; item += pairs) {
+        const VocabItem it = vocab_item(args, item);
+        for (int kb = it.kb0; kb < it.kb1; ++kb, ++g) {
+          if (!mbar_wait(&full[g % STAGES], (g / STAGES) & 1, abort_flag)) { ok = false; break; }
+          mbar_arrive_remote(&peer_ready[g % STAGES], 0);
+        }
+      }
+    }
+  } else {
+    // ---------------- epilogue: warp w has accumulator rows 32 w .. of this CTA, a row per lane ----
+    uint8_t* stage = staging + warp * 8192;
+    int n = 0, round = 0;
+    // a 32-row x 128-byte tile, 128-byte swizzled as the output maps expect, alternating two
+    auto begin_tile = [&]() {
+      if (lane == 0) bulk_wait_group_read<1>();   // the store issued two rounds ago has read its tile
+      __syncwarp();
+      return stage + (round++ & 1) * 4096;
+    };
+    auto end_tile = [&](const uint8_t* buf, const CUtensorMap* map, int x, int y, bool any) {
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        if (any) tma_store_2d(map, buf, x, y);
+        bulk_commit_group();
+      }
+    };
+    for (int item = pair; item < args.items; item += pairs, ++n) {
+      const VocabItem it = vocab_item(args, item);
+      const int buf = n & 1;
+      // (every lane of a warp goes the same way: the TMEM loads below are warp-wide)
+      if (!__all_sync(0xFFFFFFFFu, mbar_wait(&acc_full[buf], (n >> 1) & 1, abort_flag))) break;
+      tc_fence_after();
+      const uint32_t taddr = tmem_base + (static_cast<uint32_t>(warp * 32) << 16) + static_cast<uint32_t>(buf * BN);
+      const int row0 = it.m0 + rank * 128 + warp * 32, row = row0 + lane;
+      const bool rok = row < args.M;
+      auto load64 = [&](int c, uint32_t (&v)[64]) {   // columns c .. c + 63 of this lane's row
+#pragma unroll
+        for (int q = 0; q < 4; ++q) tmem_ld_16(taddr + c + 16 * q, *reinterpret_cast<uint32_t(*)[16]>(&v[16 * q]));
+        tmem_ld_wait();
+      };
+      auto drained_acc = [&]() {   // the last TMEM read of this tile is behind
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote(&acc_empty[buf], 0);
+      };
+      if (kMode == kVocabGrad) {
+        if (it.part < 0) {
+          for (int c = 0; c < BN; c += 64) {
+            uint32_t v[64];
+            load64(c, v);
+            if (c + 64 == BN) drained_acc();
+            if (it.n0 + c >= args.N) continue;
+            uint8_t* tile = begin_tile();
+            uint8_t* rowp = tile + lane * 128;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              float f[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(v[8 * k + e]);
+              *reinterpret_cast<uint4*>(rowp + ((k ^ (lane & 7)) << 4)) = pack8(f);
+            }
+            end_tile(tile, &tmOut, it.n0 + c, row0, row0 < args.M);
+          }
+        } else {
+          for (int c = 0; c < BN; c += 64) {
+            uint32_t v[64];
+            load64(c, v);
+            if (c + 64 == BN) drained_acc();
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              uint8_t* tile = begin_tile();
+              uint8_t* rowp = tile + lane * 128;
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                *reinterpret_cast<uint4*>(rowp + ((k ^ (lane & 7)) << 4)) =
+                    make_uint4(v[32 * half + 4 * k], v[32 * half + 4 * k + 1], v[32 * half + 4 * k + 2],
+                               v[32 * half + 4 * k + 3]);
+              end_tile(tile, &tmPart, c + 32 * half, it.part * BM + rank * 128 + warp * 32, true);
+            }
+          }
+        }
+        continue;
+      }
+      // ---- logits: columns behind the vocabulary read as zero products and count as -inf ----------
+      const int vcols = min(BN, args.N - it.n0);   // > 0
+      const int64_t y = rok ? __ldg(args.targets + row) : -1;
+      const bool counted = y >= 0 && y < args.N && y != args.ignore;
+      const int tcol = counted && y >= it.n0 && y < it.n0 + BN ? static_cast<int>(y - it.n0) : -1;
+      if (kMode == kVocabStats || kMode == kVocabScaled) {
+        // the target's logit, for the few rows whose target lies in this piece
+        for (unsigned left = __ballot_sync(0xFFFFFFFFu, tcol >= 0); left; left &= left - 1) {
+          const int src = __ffs(left) - 1;
+          const uint32_t v = tmem_ld_1(taddr + __shfl_sync(0xFFFFFFFFu, tcol, src));
+          tmem_ld_wait();
+          if (lane == src) args.target_logit[row] = __uint_as_float(v);
+        }
+        float m = -INFINITY;
+        for (int c = 0; c < vcols; c += 64) {
+          uint32_t v[64];
+          load64(c, v);
+#pragma unroll
+          for (int e = 0; e < 64; ++e) m = fmaxf(m, c + e < vcols ? __uint_as_float(v[e]) : -INFINITY);
+        }
+        // an infinite maximum is no reference point: exp(l) itself then sums to 0 or to infinity
+        const float ml = (fabsf(m) == INFINITY ? 0.f : m) * kLog2e;
+        float s0 = 0.f, s1 = 0.f;
+        for (int c = 0; c < BN; c += 64) {
+          if (c >= vcols && (kMode == kVocabStats || it.n0 + c >= args.ldp)) break;
+          uint32_t v[64];
+          load64(c, v);
+          float p[64];
+#pragma unroll
+          for (int e = 0; e < 64; ++e) p[e] = c + e < vcols ? ex2(fmaf(__uint_as_float(v[e]), kLog2e, -ml)) : 0.f;
+#pragma unroll
+          for (int e = 0; e < 64; e += 2) {
+            s0 += p[e];
+            s1 += p[e + 1];
+          }
+          if (kMode == kVocabScaled) {
+            uint8_t* tile = begin_tile();
+            uint8_t* rowp = tile + lane * 128;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              *reinterpret_cast<uint4*>(rowp + ((k ^ (lane & 7)) << 4)) =
+                  pack8(*reinterpret_cast<const float(*)[8]>(&p[8 * k]));
+            end_tile(tile, &tmOut, it.n0 + c, row0, row0 < args.M);
+          }
+        }
+        drained_acc();
+        if (rok) args.stats[static_cast<int64_t>(row) * args.n_tiles + it.nt] = make_float2(m, s0 + s1);
+      } else {
+        const float b = counted ? __ldg(args.dloss + row) : 0.f;
+        const float a = b + (rok && args.dlse ? __ldg(args.dlse + row) : 0.f);
+        const float nl = rok ? -__ldg(args.lse + row) * kLog2e : 0.f;
+        for (int c = 0; c < BN && it.n0 + c < args.ldp; c += 64) {
+          uint32_t v[64];
+          load64(c, v);
+          uint8_t* tile = begin_tile();
+          uint8_t* rowp = tile + lane * 128;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            float f[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const int col = c + 8 * k + e;
+              // a row that counts for nothing is zero whatever its logits are
+              f[e] = col < vcols && a != 0.f ? a * ex2(fmaf(__uint_as_float(v[8 * k + e]), kLog2e, nl)) : 0.f;
+              if (col == tcol) f[e] -= b;
+            }
+            *reinterpret_cast<uint4*>(rowp + ((k ^ (lane & 7)) << 4)) = pack8(f);
+          }
+          end_tile(tile, &tmOut, it.n0 + c, row0, row0 < args.M);
+        }
+        drained_acc();
+      }
+    }
+    if (lane == 0) bulk_wait_group<0>();   // the output is written before the CTA retires
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();   // no CTA leaves while its peer may still signal it or read its TMEM slice
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc2(tmem_base, kTmemCols);
+  }
+}
+
+// ------------------------------------------------------------------------------------------
+// rows
+// ------------------------------------------------------------------------------------------
+struct VocabRowArgs {
+  const float2* stats;        // t x n_tiles
+  const float* target_logit;
+  const int64_t* targets;
+  int64_t ignore;
+  int t, v, n_tiles;
+  float* loss;
+  float* lse;
+  // vocab_scale_kernel only
+  const float* dloss;
+  uint16_t* g;                // t x ldp
+  int ldp;
+};
+
+// Joins a row's pieces: the larger of two maxima is the new reference point, as in any running
+// softmax. A sum is zero or infinite only where all or some of its logits are infinite.
+__device__ __forceinline__ float2 join_stats(float2 p, float2 q) {
+  const float m = fmaxf(p.x, q.x);
+  const float r = fabsf(m) == INFINITY ? 0.f : m;
+  // a piece whose maximum is infinite was summed against 0, not against its maximum
+  const float pr = fabsf(p.x) == INFINITY ? 0.f : p.x, qr = fabsf(q.x) == INFINITY ? 0.f : q.x;
+  const float ps = p.y == 0.f ? 0.f : p.y * ex2((pr - r) * vg::kLog2e);
+  const float qs = q.y == 0.f ? 0.f : q.y * ex2((qr - r) * vg::kLog2e);
+  return make_float2(m, ps + qs);
+}
+
+// (loss, lse) of a row from its joined statistics.
+__device__ __forceinline__ float2 row_loss(const VocabRowArgs& a, int row, float2 st, bool& counted) {
+  const float lse = (fabsf(st.x) == INFINITY ? 0.f : st.x) + logf(st.y);
+  const int64_t y = a.targets[row];
+  const bool inside = y >= 0 && y < a.v;
+  counted = inside && y != a.ignore;
+  if (!inside && y != a.ignore) report(kDevTarget);
+  return make_float2(counted ? lse - a.target_logit[row] : 0.f, lse);
+}
+
+__device__ __forceinline__ float2 warp_join(float2 st) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    float2 q;
+    q.x = __shfl_xor_sync(0xFFFFFFFFu, st.x, o);
+    q.y = __shfl_xor_sync(0xFFFFFFFFu, st.y, o);
+    st = join_stats(st, q);
+  }
+  return st;
+}
+
+// A warp per row.
+__global__ void __launch_bounds__(256) vocab_rows_kernel(const VocabRowArgs a) {
+  const int row = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (row >= a.t) return;
+  float2 st = make_float2(-INFINITY, 0.f);
+  for (int i = lane; i < a.n_tiles; i += 32) st = join_stats(st, a.stats[static_cast<int64_t>(row) * a.n_tiles + i]);
+  st = warp_join(st);
+  if (lane == 0) {
+    bool counted;
+    const float2 r = row_loss(a, row, st, counted);
+    a.loss[row] = r.x;
+    a.lse[row] = r.y;
+  }
+}
+
+// A CTA per row: the row's loss and lse, then its scaled exponentials become g in place:
+// g_v = dloss . exp(piece's maximum - lse) . (stored exp(l_v - piece's maximum)), and at the target
+// dloss . (exp(l - lse) - 1) from the fp32 logit.
+__global__ void __launch_bounds__(256) vocab_scale_kernel(const VocabRowArgs a) {
+  __shared__ float2 sh[8];
+  __shared__ float s_lse, s_b, s_ty;
+  const int row = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const float2* stats = a.stats + static_cast<int64_t>(row) * a.n_tiles;
+  float2 st = make_float2(-INFINITY, 0.f);
+  for (int i = threadIdx.x; i < a.n_tiles; i += 256) st = join_stats(st, stats[i]);
+  st = warp_join(st);
+  if (lane == 0) sh[warp] = st;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < 8; ++w) st = join_stats(st, sh[w]);
+    bool counted;
+    const float2 r = row_loss(a, row, st, counted);
+    a.loss[row] = r.x;
+    a.lse[row] = r.y;
+    s_lse = r.y;
+    s_b = counted ? a.dloss[row] : 0.f;
+    s_ty = counted ? s_b * (ex2(-r.x * vg::kLog2e) - 1.f) : 0.f;
+  }
+  __syncthreads();
+  const float lse = s_lse, b = s_b;
+  const int64_t y = a.targets[row];
+  const int ty = y >= 0 && y < a.v && y != a.ignore ? static_cast<int>(y) : -1;
+  uint4* g = reinterpret_cast<uint4*>(a.g + static_cast<int64_t>(row) * a.ldp);
+  for (int v0 = warp * 32; v0 * 8 < a.ldp; v0 += 256) {   // a warp's 32 vectors of 8: one piece
+    const int v = v0 + lane;
+    if (v * 8 >= a.ldp) continue;
+    float f[8];
+    unpack8(g[v], f);
+    const float m = stats[v0 >> 5].x;
+    const float k = b * ex2(((fabsf(m) == INFINITY ? 0.f : m) - lse) * vg::kLog2e);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = b == 0.f ? 0.f : f[e] * k;
+    if (ty >= 0 && (ty >> 3) == v) f[ty & 7] = s_ty;
+    g[v] = pack8(f);
+  }
+}
+
+// dX tiles whose K was split: the partial tiles are added in order and rounded once.
+__global__ void __launch_bounds__(256)
+    vocab_join_kernel(const float* part, uint16_t* dX, const VocabGemmArgs a) {
+  const int tile = blockIdx.x, r = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  VocabGemmArgs b = a;
+  b.splits = 1;
+  const VocabItem it = vocab_item(b, a.whole + tile);
+  const int row = it.m0 + r, col = it.n0 + lane * 8;
+  if (row >= a.M || col >= a.N) return;   // N % 8 == 0
+  float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  for (int p = 0; p < a.splits; ++p) {
+    const float4* q = reinterpret_cast<const float4*>(
+        part + ((static_cast<int64_t>(tile) * a.splits + p) * vg::BM + r) * vg::BN + lane * 8);
+    const float4 u = __ldcg(q), w = __ldcg(q + 1);
+    s[0] += u.x; s[1] += u.y; s[2] += u.z; s[3] += u.w;
+    s[4] += w.x; s[5] += w.y; s[6] += w.z; s[7] += w.w;
+  }
+  *reinterpret_cast<uint4*>(dX + static_cast<int64_t>(row) * a.N + col) = pack8(s);
+}
+
+}  // namespace qlora

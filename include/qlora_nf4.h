@@ -429,6 +429,41 @@ QLORA_API int qlora_norm_residual_bwd(const uint16_t *dx_out, const uint16_t *dn
                                       qlora_stream_t stream);
 QLORA_API size_t qlora_norm_residual_bwd_workspace_bytes(int64_t t, int64_t h);
 
+/* Softmax cross entropy through a frozen output head, with its gradient: what a training step
+ * starts its backward from, and what scoring needs. No counterpart in the QLoRA method. The head is
+ * frozen like every base weight here and gets no gradient. With logits l = X.W^T, in fp32:
+ *   lse_i  = log sum_v exp(l_iv),   loss_i = lse_i - l_i[y_i],
+ *   dX_i   = sum_v (a_i exp(l_iv - lse_i) - b_i [v = y_i]) W_v,  b_i = dloss_i, a_i = b_i + dlse_i.
+ * The vocabulary is walked in pieces; the t x v logits are never stored. The calls with a gradient
+ * hold the bf16 factors of W_v for a bounded run of tokens (256 MiB) in the workspace at a time.
+ *   X        device bf16, t x h row-major.  8 <= h, h % 8 == 0.
+ *   W        device bf16, v x h row-major (one row per word of the vocabulary). 1 <= v <= 2^24.
+ *   targets  device int64, t, 8-byte aligned. A target equal to ignore_index is not counted: its
+ *            loss is 0 and its dloss is not used. One outside 0 .. v-1 that is not ignore_index
+ *            is treated the same and sets QLORA_DEV_TARGET (forward calls only).
+ *   loss, lse  device fp32, t each, 4-byte aligned (outputs; lse is the backward's input).
+ *   dloss    device fp32, t, 4-byte aligned: gradient of each loss (1 / count for their mean).
+ *   dlse     the same of each lse (for penalties on it), counted or not, or NULL.
+ *   dX       device bf16, t x h (output). A token whose a and b are zero gets zero.
+ *   workspace, ws_bytes: at least the matching _workspace_bytes(t, h, v).
+ * qlora_vocab_loss_fwd_bwd computes loss, lse and dX in one call for a dloss known before the loss
+ * (a mean, a sum, any weights): it forms the logits once where fwd and bwd form them twice.
+ * Errors: INVALID_ARG (NULL, t or v < 1), BAD_SHAPE, MISALIGNED, WORKSPACE, CUDA. */
+QLORA_API int qlora_vocab_loss_fwd(const uint16_t *X, const uint16_t *W, int64_t t, int64_t h, int64_t v,
+                                   const int64_t *targets, int64_t ignore_index, float *loss, float *lse,
+                                   void *workspace, size_t ws_bytes, qlora_stream_t stream);
+QLORA_API int qlora_vocab_loss_bwd(const uint16_t *X, const uint16_t *W, int64_t t, int64_t h, int64_t v,
+                                   const int64_t *targets, int64_t ignore_index, const float *lse,
+                                   const float *dloss, const float *dlse, uint16_t *dX, void *workspace,
+                                   size_t ws_bytes, qlora_stream_t stream);
+QLORA_API int qlora_vocab_loss_fwd_bwd(const uint16_t *X, const uint16_t *W, int64_t t, int64_t h, int64_t v,
+                                       const int64_t *targets, int64_t ignore_index, const float *dloss,
+                                       float *loss, float *lse, uint16_t *dX, void *workspace,
+                                       size_t ws_bytes, qlora_stream_t stream);
+QLORA_API size_t qlora_vocab_loss_fwd_workspace_bytes(int64_t t, int64_t h, int64_t v);
+QLORA_API size_t qlora_vocab_loss_bwd_workspace_bytes(int64_t t, int64_t h, int64_t v);
+QLORA_API size_t qlora_vocab_loss_fwd_bwd_workspace_bytes(int64_t t, int64_t h, int64_t v);
+
 /* Launch shape of the decode GEMV (t <= 16), a scheduling knob with no counterpart in the
  * method. By default the GEMV runs one CTA of 16 warps per SM and splits its units (32 rows x
  * 128 inputs) evenly over all their warps. qlora_set_gemv_max_ctas(n) caps that CTA count at

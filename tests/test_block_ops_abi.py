@@ -71,6 +71,37 @@ def test_norm_backward(lib):
     assert lib.qlora_norm_residual_bwd_workspace_bytes(4, 20000) == 0
 
 
+def test_vocabulary_loss(lib):
+    base = dict(X=P, W=P, t=4, h=64, v=100, y=P, ignore=-100)
+
+    def fwd(loss=P, lse=P, ws=P, n=BIG, **k):
+        return lib.qlora_vocab_loss_fwd(*{**base, **k}.values(), loss, lse, ws, n, None)
+
+    def bwd(lse=P, dloss=P, dlse=P, dX=P, ws=P, n=BIG, **k):
+        return lib.qlora_vocab_loss_bwd(*{**base, **k}.values(), lse, dloss, dlse, dX, ws, n, None)
+
+    def both(dloss=P, loss=P, lse=P, dX=P, ws=P, n=BIG, **k):
+        return lib.qlora_vocab_loss_fwd_bwd(*{**base, **k}.values(), dloss, loss, lse, dX, ws, n, None)
+    for f in (fwd, bwd, both):
+        for k in ("X", "W", "y", "lse"):
+            assert f(**{k: None}) == INVALID, (f, k)
+        assert f(t=0) == f(v=0) == INVALID
+        assert f(h=0) == f(h=12) == f(t=1 << 31) == f(v=(1 << 24) + 1) == SHAPE
+        for k in ("X", "W"):
+            assert f(**{k: P + 8}) == ALIGN
+        assert f(y=P + 4) == f(lse=P + 2) == f(ws=P + 8) == ALIGN
+        assert f(ws=None) == f(n=8) == WS
+    assert fwd(loss=None) == both(loss=None) == both(dloss=None) == bwd(dloss=None) == bwd(dX=None) == INVALID
+    assert bwd(dX=P + 8) == bwd(dlse=P + 1) == both(loss=P + 2) == ALIGN
+    for name in ("fwd", "bwd", "fwd_bwd"):
+        f = getattr(lib, f"qlora_vocab_loss_{name}_workspace_bytes")
+        assert f(4, 12, 100) == f(0, 64, 100) == f(4, 64, 0) == 0
+    # the gradient's workspace is bounded whatever the batch: 256 MiB of factors, partial tiles, statistics
+    bound = (256 << 20) + 160 * 256 * 256 * 4 + (8 << 20)
+    assert lib.qlora_vocab_loss_fwd_bwd_workspace_bytes(1 << 20, 4096, 32000) <= bound
+    assert lib.qlora_vocab_loss_bwd_workspace_bytes(1 << 20, 4096, 32000) <= bound
+
+
 def test_binding_refuses_host_tensors_shapes_and_unknown_activations():
     x = torch.zeros(4, 64, dtype=torch.bfloat16)
     p = B.PackedNF4(64, 64, "cpu")
