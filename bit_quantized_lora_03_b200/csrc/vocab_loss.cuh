@@ -113,8 +113,7 @@ __global__ void __launch_bounds__(vg::kThreads, 1)
   uint8_t* staging = smem + STAGES * STAGE_BYTES;
   uint64_t* full = reinterpret_cast<uint64_t*>(staging + kStaging);
   uint64_t* empty = full + STAGES;
-  uint64_t* peer_ready = empty + STAGES;   // even CTA: the odd CTA's stage has landed
-  uint64_t* acc_full = peer_ready + STAGES;
+  uint64_t* acc_full = empty + STAGES;
   uint64_t* acc_empty = acc_full + 2;      // even CTA: both CTAs have drained the accumulator
   uint64_t* drained = acc_empty + 2;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drained + 1);
@@ -128,7 +127,6 @@ __global__ void __launch_bounds__(vg::kThreads, 1)
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
-      mbar_init(&peer_ready[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&acc_full[b], 1);
@@ -155,6 +153,9 @@ __global__ void __launch_bounds__(vg::kThreads, 1)
 
   if (warp == kTmaWarp) {
     if (lane == 0) {
+      // both CTAs' copies count on the even CTA's barrier: the MMA issuer waits for one barrier, and
+      // no thread of the odd CTA has to pass the news on (a relay cost 930 cycles a K-step of 512)
+      const uint32_t full0 = cluster_smem_addr(full, 0);
       int g = 0;
       bool ok = true;
       for (int item = pair; ok && item < args.items; item += pairs) {
@@ -163,18 +164,26 @@ __global__ void __launch_bounds__(vg::kThreads, 1)
           const int slot = g % STAGES;
           if (!mbar_wait(&empty[slot], ((g / STAGES) & 1) ^ 1u, abort_flag)) { ok = false; break; }
           uint8_t* dst = smem + slot * STAGE_BYTES;
-          mbar_arrive_expect_tx(&full[slot], STAGE_BYTES);
-          tma_load_2d(dst, &tmA, &full[slot], kb * BK, it.m0 + rank * 128);
+          if (rank == 0) mbar_arrive_expect_tx(&full[slot], 2 * STAGE_BYTES);
+          const uint32_t bar = full0 + static_cast<uint32_t>(slot * sizeof(uint64_t));
+          tma_load_2d_pair(dst, &tmA, bar, kb * BK, it.m0 + rank * 128);
           if (!kBmn) {
-            tma_load_2d(dst + A_BYTES, &tmB, &full[slot], kb * BK, it.n0 + rank * 128);
+            tma_load_2d_pair(dst + A_BYTES, &tmB, bar, kb * BK, it.n0 + rank * 128);
           } else {
-            tma_load_2d(dst + A_BYTES, &tmB, &full[slot], it.n0 + rank * 128, kb * BK);
-            tma_load_2d(dst + A_BYTES + 8192, &tmB, &full[slot], it.n0 + rank * 128 + 64, kb * BK);
+            tma_load_2d_pair(dst + A_BYTES, &tmB, bar, it.n0 + rank * 128, kb * BK);
+            tma_load_2d_pair(dst + A_BYTES + 8192, &tmB, bar, it.n0 + rank * 128 + 64, kb * BK);
           }
         }
       }
-      if (*abort_flag)   // no copy may still be writing this CTA's shared memory when it exits
-        for (int j = (g > STAGES ? g - STAGES : 0); j < g; ++j) mbar_drain(&full[j % STAGES], (j / STAGES) & 1);
+      if (*abort_flag) {
+        // no copy may still be writing shared memory when its CTA exits: the even CTA waits for its
+        // stages (both CTAs' bytes); the odd one, whose copies count there, gives its own, at most
+        // STAGES of them, a thousand times a copy's latency (and stays until the cluster's barrier)
+        if (rank == 0)
+          for (int j = (g > STAGES ? g - STAGES : 0); j < g; ++j) mbar_drain(&full[j % STAGES], (j / STAGES) & 1);
+        else
+          for (int i = 0; i < 2000; ++i) __nanosleep(1000);
+      }
     }
   } else if (warp == kMmaWarp) {
     if (lane == 0 && rank == 0) {
@@ -189,10 +198,7 @@ __global__ void __launch_bounds__(vg::kThreads, 1)
         for (int kb = it.kb0; kb < it.kb1; ++kb, ++g) {
           const int slot = g % STAGES;
           const uint32_t ph = (g / STAGES) & 1;
-          if (!mbar_wait(&full[slot], ph, abort_flag) || !mbar_wait_cluster(&peer_ready[slot], ph, abort_flag)) {
-            ok = false;
-            break;
-          }
+          if (!mbar_wait_cluster(&full[slot], ph, abort_flag)) { ok = false; break; }
           tc_fence_after();
           const uint32_t a_addr = smem_addr(smem + slot * STAGE_BYTES), b_addr = a_addr + A_BYTES;
 #pragma unroll
@@ -208,16 +214,6 @@ __global__ void __launch_bounds__(vg::kThreads, 1)
       }
       umma2_commit_multicast(drained, 0x1);   // every MMA has read its operands before the CTAs leave
       mbar_drain(drained, 0);
-    } else if (lane == 0) {
-      int g = 0;
-      bool ok = true;
-      for (int item = pair; ok && item < args.items; item += pairs) {
-        const VocabItem it = vocab_item(args, item);
-        for (int kb = it.kb0; kb < it.kb1; ++kb, ++g) {
-          if (!mbar_wait(&full[g % STAGES], (g / STAGES) & 1, abort_flag)) { ok = false; break; }
-          mbar_arrive_remote(&peer_ready[g % STAGES], 0);
-        }
-      }
     }
   } else {
     // ---------------- epilogue: warp w has accumulator rows 32 w .. of this CTA, a row per lane ----
@@ -240,8 +236,14 @@ __global__ void __launch_bounds__(vg::kThreads, 1)
     for (int item = pair; item < args.items; item += pairs, ++n) {
       const VocabItem it = vocab_item(args, item);
       const int buf = n & 1;
-      // (every lane of a warp goes the same way: the TMEM loads below are warp-wide)
-      if (!__all_sync(0xFFFFFFFFu, mbar_wait(&acc_full[buf], (n >> 1) & 1, abort_flag))) break;
+      // One lane polls, with pauses: 128 threads polling the barrier through a whole main loop take
+      // the shared-memory bandwidth that the MMAs read their operands with.
+      bool ready = true;
+      if (lane == 0) {
+        for (int i = 0; i < 4096 && !mbar_try_wait(&acc_full[buf], (n >> 1) & 1) && !*abort_flag; ++i) __nanosleep(100);
+        ready = mbar_wait(&acc_full[buf], (n >> 1) & 1, abort_flag);
+      }
+      if (!__shfl_sync(0xFFFFFFFFu, ready, 0)) break;
       tc_fence_after();
       const uint32_t taddr = tmem_base + (static_cast<uint32_t>(warp * 32) << 16) + static_cast<uint32_t>(buf * BN);
       const int row0 = it.m0 + rank * 128 + warp * 32, row = row0 + lane;
