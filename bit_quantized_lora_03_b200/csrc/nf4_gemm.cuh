@@ -45,16 +45,21 @@ constexpr int A_HALF = 128 * BK * 2;       // 16 KB: this CTA's 128 rows of one 
 constexpr int A_BYTES = 2 * A_HALF;        // 32 KB
 constexpr int B_BYTES = BNH * BK * 2;      // 16 KB
 constexpr int P_BYTES = BNH * BK / 2;      // 4 KB of packed codes
+constexpr int P_STAGES = 8;                // their own ring: codes are read into registers and their slot
+constexpr int P_AHEAD = 4;                 // is free long before the step's MMAs, so they run steps ahead
 constexpr int kWorkWarps = 8;              // warps 0-7: dequant producers, then epilogue
+constexpr int kGroupWarps = kWorkWarps / 2;  // producers of one stage: warps 0-3 of the even K-steps,
+                                             // 4-7 of the odd ones
 constexpr int kTmaWarp = 8;
-constexpr int kMmaWarp = 9;                // even CTA: MMA issuer; odd CTA: readiness relay
+constexpr int kMmaWarp = 9;                // even CTA: MMA issuer
 constexpr int kThreads = 10 * 32;
 constexpr int kTmemCols = 512;
 constexpr int kEpiZTile = kWorkWarps * 8192;   // the staging tiles of Z lie behind those of Y
+static_assert(P_AHEAD <= P_STAGES && P_STAGES % 2 == 0, "a code slot belongs to one producer group");
 static_assert(2 * kEpiZTile <= STAGES * (A_BYTES + B_BYTES), "staging tiles in the drained stage buffers");
 
 constexpr size_t nf4_gemm_smem_bytes() {
-  return 1024 /* alignment slack */ + STAGES * (A_BYTES + B_BYTES + P_BYTES) + 256;
+  return 1024 /* alignment slack */ + STAGES * (A_BYTES + B_BYTES) + P_STAGES * P_BYTES + 384;
 }
 
 }  // namespace tc
@@ -102,10 +107,11 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
   uint8_t* sA = smem;
   uint8_t* sB = sA + STAGES * A_BYTES;
   uint8_t* sP = sB + STAGES * B_BYTES;
-  uint64_t* full_ap = reinterpret_cast<uint64_t*>(sP + STAGES * P_BYTES);
-  uint64_t* full_b = full_ap + STAGES;
-  uint64_t* peer_ready = full_b + STAGES;   // even CTA: the odd CTA's stage is complete
-  uint64_t* empty = peer_ready + STAGES;
+  uint64_t* full_a = reinterpret_cast<uint64_t*>(sP + P_STAGES * P_BYTES);  // even CTA: both CTAs' A (and LoRA B)
+  uint64_t* full_p = full_a + STAGES;       // this CTA's packed codes
+  uint64_t* empty_p = full_p + P_STAGES;
+  uint64_t* full_b = empty_p + P_STAGES;    // even CTA: both CTAs' dequantized B
+  uint64_t* empty = full_b + STAGES;
   uint64_t* acc_full = empty + STAGES;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(acc_full + 1);
   volatile uint32_t* abort_flag = tmem_holder + 1;
@@ -123,10 +129,13 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(&full_ap[s], 1);
-      mbar_init(&full_b[s], kWorkWarps * 32);
-      mbar_init(&peer_ready[s], 1);
+      mbar_init(&full_a[s], 1);
+      mbar_init(&full_b[s], 2 * kGroupWarps);
       mbar_init(&empty[s], 1);
+    }
+    for (int s = 0; s < P_STAGES; ++s) {
+      mbar_init(&full_p[s], 1);
+      mbar_init(&empty_p[s], kGroupWarps);
     }
     mbar_init(acc_full, 1);
     *abort_flag = 0u;
@@ -151,47 +160,67 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
 
   if (warp == kTmaWarp) {
     if (lane == 0) {
-      int issued = 0;
+      // What the MMA reads is counted on barriers of the even CTA, whose thread issues it, for both
+      // CTAs: the odd CTA's copies and dequantized tiles arrive there directly.
+      const uint32_t full_a0 = cluster_smem_addr(full_a, 0);
+      int issued = 0, codes = 0;   // K-steps whose operand, and whose code, copies were issued
+      auto load_codes = [&](int kb) {
+        const int slot = kb % P_STAGES;
+        if (!mbar_wait(&empty_p[slot], ((kb / P_STAGES) & 1) ^ 1u, abort_flag)) return false;
+        mbar_arrive_expect_tx(&full_p[slot], P_BYTES);
+        if (!kBwd) {
+          tma_load_2d(sP + slot * P_BYTES, &tmP, &full_p[slot], kb * (BK / 2), nh0);
+        } else {
+          tma_load_2d(sP + slot * P_BYTES, &tmP, &full_p[slot], nh0 / 2, kb * BK);
+          tma_load_2d(sP + slot * P_BYTES + 2048, &tmP, &full_p[slot], nh0 / 2 + 32, kb * BK);
+        }
+        codes = kb + 1;
+        return true;
+      };
+      for (int kb = 0; kb < P_AHEAD && kb < args.num_kb; ++kb) load_codes(kb);   // (free slots: no wait)
       for (int i = 0; i < total; ++i) {
         const int slot = i % STAGES;
         const uint32_t ph = (i / STAGES) & 1;
+        if (i + P_AHEAD < args.num_kb && !load_codes(i + P_AHEAD)) break;
         if (!mbar_wait(&empty[slot], ph ^ 1u, abort_flag)) break;
         uint8_t* a_dst = sA + slot * A_BYTES;
         uint8_t* b_dst = sB + slot * B_BYTES;
+        const uint32_t bar = full_a0 + static_cast<uint32_t>(slot * sizeof(uint64_t));
         if (i >= args.num_kb) {
           // sT / sU come from the kernel launched just before this one, which may still be
           // running (programmatic dependent launch): wait for it before the first LoRA load
           if (i == args.num_kb) pdl_wait();
           const int li = i - args.num_kb;
-          mbar_arrive_expect_tx(&full_ap[slot], A_BYTES + B_BYTES);
-          tma_load_2d(a_dst, &tmA2, &full_ap[slot], li * BK, mrow);
-          tma_load_2d(a_dst + A_HALF, &tmA2, &full_ap[slot], li * BK, mrow + 256);
+          if (rank == 0) mbar_arrive_expect_tx(&full_a[slot], 2 * (A_BYTES + B_BYTES));
+          tma_load_2d_pair(a_dst, &tmA2, bar, li * BK, mrow);
+          tma_load_2d_pair(a_dst + A_HALF, &tmA2, bar, li * BK, mrow + 256);
           if (!kBwd) {
             // L2 (r x o), MN-major B: this CTA's two 64-column atoms, 8 KB apart
-            tma_load_2d(b_dst, &tmB2, &full_ap[slot], nh0, li * BK);
-            tma_load_2d(b_dst + 8192, &tmB2, &full_ap[slot], nh0 + 64, li * BK);
+            tma_load_2d_pair(b_dst, &tmB2, bar, nh0, li * BK);
+            tma_load_2d_pair(b_dst + 8192, &tmB2, bar, nh0 + 64, li * BK);
           } else {
             // L1 (h x r), K-major B: this CTA's 128 rows of 64 ranks
-            tma_load_2d(b_dst, &tmB2, &full_ap[slot], li * BK, nh0);
+            tma_load_2d_pair(b_dst, &tmB2, bar, li * BK, nh0);
           }
         } else {
           const int kb = i;
-          mbar_arrive_expect_tx(&full_ap[slot], A_BYTES + P_BYTES);
-          tma_load_2d(a_dst, &tmA, &full_ap[slot], kb * BK, mrow);
-          tma_load_2d(a_dst + A_HALF, &tmA, &full_ap[slot], kb * BK, mrow + 256);
-          if (!kBwd) {
-            tma_load_2d(sP + slot * P_BYTES, &tmP, &full_ap[slot], kb * (BK / 2), nh0);
-          } else {
-            tma_load_2d(sP + slot * P_BYTES, &tmP, &full_ap[slot], nh0 / 2, kb * BK);
-            tma_load_2d(sP + slot * P_BYTES + 2048, &tmP, &full_ap[slot], nh0 / 2 + 32, kb * BK);
-          }
+          if (rank == 0) mbar_arrive_expect_tx(&full_a[slot], 2 * A_BYTES);
+          tma_load_2d_pair(a_dst, &tmA, bar, kb * BK, mrow);
+          tma_load_2d_pair(a_dst + A_HALF, &tmA, bar, kb * BK, mrow + 256);
         }
         issued = i + 1;
       }
       if (*abort_flag) {
-        // make sure no copy is still writing this CTA's shared memory before it exits
-        for (int j = (issued > STAGES ? issued - STAGES : 0); j < issued; ++j)
-          mbar_drain(&full_ap[j % STAGES], (j / STAGES) & 1);
+        // make sure no copy is still writing this CTA's shared memory before it exits: the odd
+        // CTA's A copies count on its peer's barriers, so it gives them, at most STAGES of them, a
+        // thousand times a copy's latency (and stays until the cluster's barrier below)
+        for (int j = (issued > STAGES ? issued - STAGES : 0); j < issued; ++j) {
+          if (rank == 0) mbar_drain(&full_a[j % STAGES], (j / STAGES) & 1);
+        }
+        for (int j = (codes > P_STAGES ? codes - P_STAGES : 0); j < codes; ++j)
+          mbar_drain(&full_p[j % P_STAGES], (j / P_STAGES) & 1);
+        if (rank != 0)
+          for (int j = 0; j < 2000; ++j) __nanosleep(1000);
       }
     }
   } else if (warp == kMmaWarp) {
@@ -203,9 +232,8 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
       for (int i = 0; i < total; ++i) {
         const int slot = i % STAGES;
         const uint32_t ph = (i / STAGES) & 1;
-        if (!mbar_wait(&full_ap[slot], ph, abort_flag)) break;
+        if (!mbar_wait(&full_a[slot], ph, abort_flag)) break;
         if (!mbar_wait(&full_b[slot], ph, abort_flag)) break;
-        if (!mbar_wait_cluster(&peer_ready[slot], ph, abort_flag)) break;
         tc_fence_after();
         const bool lora = i >= args.num_kb;
         const bool b_mn = lora ? !kBwd : kBwd;
@@ -228,25 +256,19 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
       // completes in both CTAs once every MMA above has finished (also after an abort)
       umma2_commit_multicast(acc_full, 0x3);
       if (*abort_flag && any) mbar_drain(acc_full, 0);
-    } else if (lane == 0) {
-      // odd CTA: tell the issuer when this CTA's half of each stage is in shared memory
-      for (int i = 0; i < total; ++i) {
-        const int slot = i % STAGES;
-        const uint32_t ph = (i / STAGES) & 1;
-        if (!mbar_wait(&full_ap[slot], ph, abort_flag)) break;
-        if (!mbar_wait(&full_b[slot], ph, abort_flag)) break;
-        mbar_arrive_remote(&peer_ready[slot], 0);
-      }
     }
   } else {
-    // ---------------- warps 0-7: dequant producers (half a 64-weight block per thread per
-    // stage: 128 blocks of this CTA's 128 columns), then the epilogue -----------------------
+    // ---------------- warps 0-7: dequant producers (a 64-weight block per thread per stage: 128
+    // blocks of this CTA's 128 columns), then the epilogue -----------------------------------
+    // Two groups of four warps take alternate K-steps: a step's chain of waits, table, selects and
+    // stores is longer than its MMAs, so that one group alone, or all eight warps on every step,
+    // would set the pace (and a thread builds a block's table once, not two threads each).
     uint64_t lv2[8];                 // the 16 fp32 levels as pairs (2i low, 2i+1 high)
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       asm("mov.b64 %0, {%1, %2};" : "=l"(lv2[i]) : "f"(args.tab.level[2 * i]), "f"(args.tab.level[2 * i + 1]));
-    const int p = threadIdx.x;       // 0..255
-    const int blk = p >> 1, half = p & 1;
+    const int group = warp / kGroupWarps;
+    const int blk = threadIdx.x & (kGroupWarps * 32 - 1);   // 0..127
     const int64_t nblk_row = args.h / kBlock;
     int64_t qbase, qstep;       // q8 index of this thread's block at weight K-step kb: qbase + kb*qstep
     int out_off, pk_off, swz;
@@ -257,7 +279,7 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
       valid = j < args.N;
       qbase = j * nblk_row;
       qstep = 1;
-      pk_off = blk * 32 + half * 16;
+      pk_off = blk * 32;
       out_off = (blk >> 3) * 1024 + (blk & 7) * 128;
       swz = blk & 7;
     } else {
@@ -266,58 +288,66 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
       valid = (nh0 + a * 64) < args.N;
       qbase = static_cast<int64_t>(jl) * nblk_row + (nh0 / 64) + a;
       qstep = 64 * nblk_row;
-      pk_off = a * 2048 + jl * 32 + half * 16;
+      pk_off = a * 2048 + jl * 32;
       out_off = a * 8192 + (jl >> 3) * 1024 + (jl & 7) * 128;
       swz = jl & 7;
     }
-    // 8-bit scale and second-level scale of this thread's block, fetched kPf stages ahead into
+    // 8-bit scale and second-level scale of this thread's block, fetched kPf of its steps ahead into
     // a ring of registers; the loop below is unrolled by kPf so that every ring index is a
-    // compile-time constant and a load is waited for only when its stage comes up
+    // compile-time constant and a load is waited for only when its step comes up
     constexpr int kPf = 4;
     const int nk = args.num_kb;
     uint32_t qr[kPf];
     float sr[kPf];
 #pragma unroll
     for (int j = 0; j < kPf; ++j) {
+      const int i = 2 * j + group;
       qr[j] = 0u;
       sr[j] = 0.f;
-      if (valid && j < nk) {
-        const int64_t qi = qbase + static_cast<int64_t>(j) * qstep;
+      if (valid && i < nk) {
+        const int64_t qi = qbase + static_cast<int64_t>(i) * qstep;
         qr[j] = __ldg(args.q8 + qi);
         sr[j] = __ldg(args.s2 + (qi >> 8));
       }
     }
     bool ok = true;
-    for (int i0 = 0; i0 < total && ok; i0 += kPf) {
+    for (int i0 = group; i0 < total && ok; i0 += 2 * kPf) {
 #pragma unroll
       for (int j = 0; j < kPf; ++j) {
-        const int i = i0 + j;
+        const int i = i0 + 2 * j;
         if (i >= total || !ok) break;
         const int slot = i % STAGES;
         const uint32_t ph = (i / STAGES) & 1;
-        if (!mbar_wait(&empty[slot], ph ^ 1u, abort_flag)) { ok = false; break; }
         if (i < nk) {
+          // codes and table first: they do not depend on the operand slot's MMAs
           const float k = __fmul_rn(static_cast<float>(qr[j]), sr[j]);
-          if (valid && i + kPf < nk) {
-            const int64_t qi = qbase + static_cast<int64_t>(i + kPf) * qstep;
+          if (valid && i + 2 * kPf < nk) {
+            const int64_t qi = qbase + static_cast<int64_t>(i + 2 * kPf) * qstep;
             qr[j] = __ldg(args.q8 + qi);
             sr[j] = __ldg(args.s2 + (qi >> 8));
           }
-          if (!mbar_wait(&full_ap[slot], ph, abort_flag)) { ok = false; break; }
+          const int pslot = i % P_STAGES;
+          if (!mbar_wait_warp(&full_p[pslot], (i / P_STAGES) & 1, abort_flag)) { ok = false; break; }
+          const uint4* cp = reinterpret_cast<const uint4*>(sP + pslot * P_BYTES + pk_off);
+          const uint4 c0 = cp[0], c1 = cp[1];
+          __syncwarp();   // every lane has its codes
+          if (lane == 0) mbar_arrive(&empty_p[pslot]);
+          const ProdTab tab = build_prod_tab(lv2, k);
+          if (!mbar_wait_warp(&empty[slot], ph ^ 1u, abort_flag)) { ok = false; break; }
           if (valid) {
-            const ProdTab tab = build_prod_tab(lv2, k);
-            const uint4 c = *reinterpret_cast<const uint4*>(sP + slot * P_BYTES + pk_off);
-            const uint32_t words[4] = {c.x, c.y, c.z, c.w};
+            const uint32_t words[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
             uint8_t* dst = sB + slot * B_BYTES + out_off;
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              const int ch = half * 4 + u;   // 16-byte chunk (8 weights) within the 128-byte row
-              *reinterpret_cast<uint4*>(dst + ((ch ^ swz) << 4)) = dequant8_tab(words[u], tab);
-            }
+            for (int ch = 0; ch < 8; ++ch)   // 16-byte chunk (8 weights) within the 128-byte row
+              *reinterpret_cast<uint4*>(dst + ((ch ^ swz) << 4)) = dequant8_tab(words[ch], tab);
           }
           fence_proxy_async_smem();
+        } else if (!mbar_wait_warp(&empty[slot], ph ^ 1u, abort_flag)) {
+          ok = false;
+          break;
         }
-        mbar_arrive(&full_b[slot]);
+        __syncwarp();   // (each lane has fenced its own writes)
+        if (lane == 0) mbar_arrive_pair(&full_b[slot], 0);
       }
     }
 
@@ -329,9 +359,9 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
     // one TMA store of the tile: whole 128-byte lines instead of 32 scattered row pieces per
     // store instruction. Two staging tiles per warp (8 KB, in the drained stage buffers) let a
     // round's shared-memory writes overlap the previous round's store.
-    const bool done = mbar_wait(acc_full, 0, abort_flag);
+    const bool done = mbar_wait_warp(acc_full, 0, abort_flag);
     tc_fence_after();
-    if (done && !*abort_flag) {
+    if (__shfl_sync(0xFFFFFFFFu, done && !*abort_flag, 0)) {
       if (args.addend) pdl_wait();
       const int acc = warp >> 2, quad = warp & 3;
       const int row0 = mrow + acc * 256 + quad * 32;

@@ -91,6 +91,15 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity,
   }
 }
 
+// mbar_wait for a whole warp: lane 0 polls (32 lanes polling one barrier take shared-memory
+// bandwidth from the tensor core's operand reads) and every lane gets its result, so that the
+// warp goes one way whatever it is.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, volatile uint32_t* abort_flag) {
+  bool ok = true;
+  if ((threadIdx.x & 31) == 0) ok = mbar_wait(bar, parity, abort_flag);
+  return __shfl_sync(0xFFFFFFFFu, ok, 0);
+}
+
 // ------------------------------------------------------------------------------------------
 // Thread-block clusters (used by the 2-CTA tensor-core path; no TMA multicast anywhere)
 // ------------------------------------------------------------------------------------------
@@ -112,6 +121,16 @@ __device__ __forceinline__ void mbar_arrive_remote(uint64_t* bar, uint32_t rank)
   uint32_t raddr;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(raddr) : "r"(smem_addr(bar)), "r"(rank));
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(raddr) : "memory");
+}
+
+// The same arrive with release at CTA scope, for an arrive that orders only what its thread did in
+// its own shared memory or tensor memory (whose one copy every reader uses): the cluster-scope
+// release above also waits for the thread's global writes, some 1400 cycles, which is longer than
+// a K-step's MMAs.
+__device__ __forceinline__ void mbar_arrive_pair(uint64_t* bar, uint32_t rank) {
+  uint32_t raddr;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(raddr) : "r"(smem_addr(bar)), "r"(rank));
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(raddr) : "memory");
 }
 
 // Loads from the same shared-memory offset in CTA `rank` of this cluster (distributed

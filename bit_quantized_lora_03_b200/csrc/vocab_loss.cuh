@@ -193,12 +193,12 @@ __global__ void __launch_bounds__(vg::kThreads, 1)
       for (int item = pair; ok && item < args.items; item += pairs, ++n) {
         const VocabItem it = vocab_item(args, item);
         const int buf = n & 1;
-        if (!mbar_wait_cluster(&acc_empty[buf], ((n >> 1) & 1) ^ 1u, abort_flag)) break;
+        if (!mbar_wait(&acc_empty[buf], ((n >> 1) & 1) ^ 1u, abort_flag)) break;
         tc_fence_after();
         for (int kb = it.kb0; kb < it.kb1; ++kb, ++g) {
           const int slot = g % STAGES;
           const uint32_t ph = (g / STAGES) & 1;
-          if (!mbar_wait_cluster(&full[slot], ph, abort_flag)) { ok = false; break; }
+          if (!mbar_wait(&full[slot], ph, abort_flag)) { ok = false; break; }
           tc_fence_after();
           const uint32_t a_addr = smem_addr(smem + slot * STAGE_BYTES), b_addr = a_addr + A_BYTES;
 #pragma unroll
@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(vg::kThreads, 1)
       auto drained_acc = [&]() {   // the last TMEM read of this tile is behind
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_remote(&acc_empty[buf], 0);
+        if (lane == 0) mbar_arrive_pair(&acc_empty[buf], 0);
       };
       if (kMode == kVocabGrad) {
         if (it.part < 0) {
