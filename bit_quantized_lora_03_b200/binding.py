@@ -120,6 +120,8 @@ def library_path() -> str:
 def lib() -> ctypes.CDLL:
     """Load the in-tree library (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             path = library_path()
@@ -418,6 +420,12 @@ def qlora_linear_bwd_dropout(dY: torch.Tensor, X: torch.Tensor, p: PackedNF4, L1
 _NO_GUARD = contextlib.nullcontext()
 
 
+def _current(dev) -> int:
+    """The current stream of `dev` as a handle (without building a torch.cuda.Stream, which took a
+    quarter of a short call's host time)."""
+    return torch._C._cuda_getCurrentRawStream(dev.index)
+
+
 def _guard(t: torch.Tensor, stream):
     """Makes the device of `t`, and `stream` if given, current for the call."""
     if not t.is_cuda:
@@ -426,7 +434,7 @@ def _guard(t: torch.Tensor, stream):
         if stream.device != t.device:
             raise ValueError(f"stream of {stream.device} for tensors on {t.device}")
         return torch.cuda.stream(stream)
-    return _NO_GUARD if torch.cuda.current_device() == t.device.index else torch.cuda.device(t.device)
+    return _NO_GUARD if torch._C._cuda_getDevice() == t.device.index else torch.cuda.device(t.device)
 
 
 def _on(dev, t: torch.Tensor | None, dtype, shape, name: str) -> int | None:
@@ -501,7 +509,7 @@ def qlora_linear_fwd_epilogue(X: torch.Tensor, p: PackedNF4, L1: torch.Tensor, L
         d = p.desc()
         _check(lib().qlora_linear_fwd_epilogue(
             ins[0], t, ctypes.byref(d), ins[1], ins[2], r, float(s), ins[3], _act_id(act), ins[4],
-            Y.data_ptr(), _ptr(Z), _ptr(sT), ws.data_ptr(), ws.numel(), _stream()),
+            Y.data_ptr(), _ptr(Z), _ptr(sT), ws.data_ptr(), ws.numel(), _current(dev)),
             "qlora_linear_fwd_epilogue")
     return Y, Z, sT
 
@@ -520,7 +528,7 @@ def qlora_epilogue_bwd(dY: torch.Tensor, Z: torch.Tensor | None, act="none",
         if dbias is not None:
             ws = _scratch(dev, ws, int(lib().qlora_epilogue_bwd_workspace_bytes(t, o)))
         _check(lib().qlora_epilogue_bwd(a, z, t, o, _act_id(act), _ptr(dZ), _ptr(dbias), _ptr(ws),
-                                        0 if ws is None else ws.numel(), _stream()),
+                                        0 if ws is None else ws.numel(), _current(dev)),
                "qlora_epilogue_bwd")
     return dZ, dbias
 
@@ -552,7 +560,7 @@ def qlora_norm_residual_fwd(x: torch.Tensor, y: torch.Tensor | None = None,
         ro = torch.empty(t, dtype=torch.float32, device=dev) if want_rstd and wo else None
         ri = torch.empty(t, dtype=torch.float32, device=dev) if want_rstd and wi else None
         _check(lib().qlora_norm_residual_fwd(xp, yp, t, h, wo, gp, rows, float(scale), wi, float(eps),
-                                             x_out.data_ptr(), _ptr(n), _ptr(ro), _ptr(ri), _stream()),
+                                             x_out.data_ptr(), _ptr(n), _ptr(ro), _ptr(ri), _current(dev)),
                "qlora_norm_residual_fwd")
     return x_out, n, ro, ri
 
@@ -588,7 +596,7 @@ def qlora_norm_residual_bwd(dx_out: torch.Tensor | None, dn: torch.Tensor | None
         ws = _scratch(dev, ws, int(lib().qlora_norm_residual_bwd_workspace_bytes(t, h)))
         _check(lib().qlora_norm_residual_bwd(*g, t, h, wo, gp, rows, float(scale), wi, ro, ri, dx.data_ptr(),
                                              _ptr(dy), _ptr(dwo), _ptr(dg), _ptr(dwi), ws.data_ptr(),
-                                             ws.numel(), _stream()),
+                                             ws.numel(), _current(dev)),
                "qlora_norm_residual_bwd")
         if dn is None and w_pre is not None:
             dwi = torch.zeros(h, dtype=f32, device=dev)
@@ -613,7 +621,7 @@ def qlora_vocab_loss_fwd(X: torch.Tensor, W: torch.Tensor, targets: torch.Tensor
         loss, lse = _out(dev, loss, f32, (t,), "loss"), _out(dev, lse, f32, (t,), "lse")
         ws = _scratch(dev, ws, int(lib().qlora_vocab_loss_fwd_workspace_bytes(t, h, v)))
         _check(lib().qlora_vocab_loss_fwd(*args, int(ignore_index), loss.data_ptr(), lse.data_ptr(),
-                                          ws.data_ptr(), ws.numel(), _stream()), "qlora_vocab_loss_fwd")
+                                          ws.data_ptr(), ws.numel(), _current(dev)), "qlora_vocab_loss_fwd")
     return loss, lse
 
 
@@ -629,7 +637,7 @@ def qlora_vocab_loss_bwd(X: torch.Tensor, W: torch.Tensor, targets: torch.Tensor
         dX = _out(dev, dX, torch.bfloat16, (t, h), "dX")
         ws = _scratch(dev, ws, int(lib().qlora_vocab_loss_bwd_workspace_bytes(t, h, v)))
         _check(lib().qlora_vocab_loss_bwd(*args, int(ignore_index), *grads, dX.data_ptr(), ws.data_ptr(),
-                                          ws.numel(), _stream()), "qlora_vocab_loss_bwd")
+                                          ws.numel(), _current(dev)), "qlora_vocab_loss_bwd")
     return dX
 
 
@@ -647,7 +655,7 @@ def qlora_vocab_loss_fwd_bwd(X: torch.Tensor, W: torch.Tensor, targets: torch.Te
         dX = _out(dev, dX, torch.bfloat16, (t, h), "dX")
         ws = _scratch(dev, ws, int(lib().qlora_vocab_loss_fwd_bwd_workspace_bytes(t, h, v)))
         _check(lib().qlora_vocab_loss_fwd_bwd(*args, int(ignore_index), d, loss.data_ptr(), lse.data_ptr(),
-                                              dX.data_ptr(), ws.data_ptr(), ws.numel(), _stream()),
+                                              dX.data_ptr(), ws.data_ptr(), ws.numel(), _current(dev)),
                "qlora_vocab_loss_fwd_bwd")
     return loss, lse, dX
 

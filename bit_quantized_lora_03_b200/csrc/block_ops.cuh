@@ -48,25 +48,20 @@ struct NormBwdPlan {
   int threads, ctas, units;   // CTAs, and runs of rows (warps for short rows, else CTAs)
   size_t smem;
 };
-constexpr int kNormCtasPerSm = 4;
+// Threads of a row at two vectors of 8 each.
+unsigned norm_threads(int64_t h) { return static_cast<unsigned>(((h / 8 + 1) / 2 + 31) / 32 * 32); }
+
 NormBwdPlan plan_norm_bwd(int64_t t, int64_t h, int sms) {
   NormBwdPlan p{};
-  if (h <= nr::kWarpRowH) {
-    constexpr int wpc = nr::kWarpRowThreads / 32;
-    p.threads = nr::kWarpRowThreads;
-    p.ctas = static_cast<int>(std::min<int64_t>((t + wpc - 1) / wpc, static_cast<int64_t>(sms) * 2));
-    p.units = p.ctas * wpc;
-    p.smem = static_cast<size_t>(wpc) * h * 4;
-  } else {
-    const int64_t vecs = h / 8;
-    const bool two = vecs > 1024;
-    p.threads = static_cast<int>(((two ? (vecs + 1) / 2 : vecs) + 31) / 32 * 32);
-    // as many CTAs as an SM's threads hold at the kernel's 64 registers a thread
-    const int per_sm = two ? 1 : std::max(1, std::min(kNormCtasPerSm, 1024 / p.threads));
-    p.ctas = static_cast<int>(std::min<int64_t>(t, static_cast<int64_t>(sms) * per_sm));
-    p.units = p.ctas;
-    p.smem = two ? static_cast<size_t>(h) * 3 * 4 : 0;
-  }
+  constexpr int wpc = nr::kWarpRowThreads / 32;
+  const bool warp_row = h <= nr::kWarpRowH, wide = h > nr::kStayH;
+  p.threads = warp_row ? nr::kWarpRowThreads : static_cast<int>(norm_threads(h));
+  // CTAs that fit an SM by threads (128 registers each); their rings and sums take
+  // 512 threads x (3 rows x 4 + 2) x 32 bytes = 224 KB of its shared memory together
+  const int per_sm = std::max(1, std::min(8, 512 / p.threads));
+  p.ctas = static_cast<int>(std::min<int64_t>(warp_row ? (t + wpc - 1) / wpc : t, static_cast<int64_t>(sms) * per_sm));
+  p.units = warp_row ? p.ctas * wpc : p.ctas;
+  p.smem = static_cast<size_t>(p.threads) * 64 * (wide ? 3 : 1 + 2 * nr::kBwdStages);
   return p;
 }
 
@@ -372,24 +367,31 @@ int qlora_norm_residual_fwd(const uint16_t* x, const uint16_t* y, int64_t t, int
   a.eps = eps;
   {
     prof::Scope ps(prof::kNorm, st);
-    if (h <= nr::kWarpRowH) {
-      constexpr int wpc = nr::kWarpRowThreads / 32;
-      const unsigned grid = static_cast<unsigned>((t + wpc - 1) / wpc);
-      if (h <= 256)
-        norm_residual_fwd_kernel<1, true><<<grid, nr::kWarpRowThreads, 0, st>>>(a);
+    const int sms = sm_count(dev);
+    constexpr int wpc = nr::kWarpRowThreads / 32;
+    const bool warp_row = h <= nr::kWarpRowH;
+    const unsigned threads = warp_row ? nr::kWarpRowThreads : norm_threads(h);
+    const int64_t rows = warp_row ? (t + wpc - 1) / wpc : t;   // CTAs' worth of rows
+    // CTAs that fit an SM by threads (up to 128 registers each; the rings take 128 KB together). With two
+    // rounds of rows for each they stay and prefetch; with fewer, a row's own latency is all there is,
+    // and a row with one vector per thread is the shortest way through it.
+    const int64_t wave = static_cast<int64_t>(sms) * std::max(1u, std::min(8u, 512u / threads));
+    const size_t smem = static_cast<size_t>(nr::kFwdStages) * 2 * 2 * threads * 16;
+    if (h <= nr::kStayH && rows >= 2 * wave) {
+      const unsigned grid = static_cast<unsigned>(wave);
+      if (warp_row)
+        norm_residual_fwd_kernel<2, true, true><<<grid, threads, smem, st>>>(a);
+      else if (y && w_post && w_pre && x_out && h == 16 * static_cast<int64_t>(threads))
+        norm_residual_fwd_kernel<2, false, true, true><<<grid, threads, smem, st>>>(a);
       else
-        norm_residual_fwd_kernel<2, true><<<grid, nr::kWarpRowThreads, 0, st>>>(a);
+        norm_residual_fwd_kernel<2, false, true><<<grid, threads, smem, st>>>(a);
+    } else if (warp_row) {
+      norm_residual_fwd_kernel<2, true, false><<<static_cast<unsigned>(rows), threads, 0, st>>>(a);
+    } else if (h <= 8192) {
+      norm_residual_fwd_kernel<1, false, false>
+          <<<static_cast<unsigned>(rows), static_cast<unsigned>((h / 8 + 31) / 32 * 32), 0, st>>>(a);
     } else {
-      // vectors of 8 per thread: one while the card has threads to spare for the rows there are
-      // (a shorter way through the row), else two, which keeps more loads of a thread in flight
-      const int64_t vecs = h / 8;
-      const bool two = vecs > 1024 || (vecs >= 256 && t >= 2 * sm_count(dev));
-      const unsigned threads = static_cast<unsigned>(((two ? (vecs + 1) / 2 : vecs) + 31) / 32 * 32);
-      const unsigned grid = static_cast<unsigned>(t);
-      if (two)
-        norm_residual_fwd_kernel<2, false><<<grid, threads, 0, st>>>(a);
-      else
-        norm_residual_fwd_kernel<1, false><<<grid, threads, 0, st>>>(a);
+      norm_residual_fwd_kernel<2, false, false><<<static_cast<unsigned>(rows), threads, 0, st>>>(a);
     }
   }
   return launch_status();
@@ -454,18 +456,19 @@ int qlora_norm_residual_bwd(const uint16_t* dx_out, const uint16_t* dn, const ui
   {
     prof::Scope ps(prof::kNorm, st);
     const unsigned grid = static_cast<unsigned>(pl.ctas), threads = static_cast<unsigned>(pl.threads);
-    if (h <= 256)
-      norm_residual_bwd_kernel<1, true><<<grid, threads, pl.smem, st>>>(a);
-    else if (h <= nr::kWarpRowH)
-      norm_residual_bwd_kernel<2, true><<<grid, threads, pl.smem, st>>>(a);
-    else if (h <= 8192)
-      norm_residual_bwd_kernel<1, false><<<grid, threads, pl.smem, st>>>(a);
+    if (h <= nr::kWarpRowH)
+      norm_residual_bwd_kernel<true, false><<<grid, threads, pl.smem, st>>>(a);
+    else if (h <= nr::kStayH && dx_out && dn && w_post && h == 16 * static_cast<int64_t>(threads))
+      norm_residual_bwd_kernel<false, false, true><<<grid, threads, pl.smem, st>>>(a);
+    else if (h <= nr::kStayH)
+      norm_residual_bwd_kernel<false, false><<<grid, threads, pl.smem, st>>>(a);
     else
-      norm_residual_bwd_kernel<2, false><<<grid, threads, pl.smem, st>>>(a);
+      norm_residual_bwd_kernel<false, true><<<grid, threads, pl.smem, st>>>(a);
   }
   if ((rc = launch_status())) return rc;
   // gate rows are shared between units unless every unit's run starts a new one
-  const int gate_blocks = gate && a.rows_per_gate > 1 && pl.units > 1 ? std::min(16, (pl.units + 6) / 8) : 0;
+  const int gate_blocks =
+      gate && a.rows_per_gate > 1 && pl.units > 1 ? std::min(64, (a.t - 1) / a.rows_per_gate + 1) : 0;
   float* pre = pl.ctas > 1 ? dw_pre : nullptr;
   float* post = pl.ctas > 1 ? dw_post : nullptr;
   if (!pre && !post && !gate_blocks) return QLORA_OK;

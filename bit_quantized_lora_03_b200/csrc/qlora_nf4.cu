@@ -149,8 +149,16 @@ Nf4Buckets device_buckets(int id = 0) {
 // Shared-memory limits of the kernels launched from block_ops.cuh.
 bool block_ops_attributes() {
   bool fine = true;
-  fine &= cudaFuncSetAttribute(norm_residual_bwd_kernel<2, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               nr::kMaxH * 3 * 4) == cudaSuccess;
+  for (auto* kernel : {norm_residual_bwd_kernel<true, false>, norm_residual_bwd_kernel<false, false>,
+                       norm_residual_bwd_kernel<false, false, true>})
+    fine &= cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 512 * 64 * (1 + 2 * nr::kBwdStages)) == cudaSuccess;
+  fine &= cudaFuncSetAttribute(norm_residual_bwd_kernel<false, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               1024 * 64 * 3) == cudaSuccess;
+  for (auto* kernel : {norm_residual_fwd_kernel<2, true, true>, norm_residual_fwd_kernel<2, false, true>,
+                       norm_residual_fwd_kernel<2, false, true, true>})
+    fine &= cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 nr::kFwdStages * 4 * 512 * 16) == cudaSuccess;
   for (auto* kernel : {vocab_gemm_kernel<kVocabStats>, vocab_gemm_kernel<kVocabScaled>,
                        vocab_gemm_kernel<kVocabProb>, vocab_gemm_kernel<kVocabGrad>})
     fine &= cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
