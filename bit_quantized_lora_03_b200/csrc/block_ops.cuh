@@ -80,7 +80,7 @@ struct VocabPlan {
   int64_t run;      // tokens per run
   int64_t ldp;      // v rounded up to 64
   int64_t n_tiles;  // pieces of the vocabulary
-  size_t g_bytes, stats_bytes, target_bytes, part_bytes;
+  size_t g_bytes, stats_bytes, row_bytes, part_bytes;   // row_bytes: one float per token of a run
 };
 VocabPlan plan_vocab(int64_t t, int64_t v, bool stats, bool grad) {
   VocabPlan p{};
@@ -94,7 +94,7 @@ VocabPlan plan_vocab(int64_t t, int64_t v, bool stats, bool grad) {
   }
   if (stats) {
     p.stats_bytes = align256(static_cast<size_t>(p.run) * p.n_tiles * 8);
-    p.target_bytes = align256(static_cast<size_t>(p.run) * 4);
+    p.row_bytes = align256(static_cast<size_t>(p.run) * 4);
   }
   return p;
 }
@@ -108,7 +108,7 @@ int check_vocab_shape(int64_t t, int64_t h, int64_t v) {
 size_t vocab_ws_bytes(int64_t t, int64_t h, int64_t v, bool stats, bool grad) {
   if (check_vocab_shape(t, h, v) != QLORA_OK) return 0;
   const VocabPlan p = plan_vocab(t, v, stats, grad);
-  return p.g_bytes + p.stats_bytes + p.target_bytes + p.part_bytes;
+  return p.g_bytes + p.part_bytes + p.stats_bytes + 3 * p.row_bytes + 256;
 }
 
 // Tiles, their order and their split. Pairs walk the list in steps; row tiles are walked in groups
@@ -190,7 +190,11 @@ int vocab_core(const VocabCall& c, void* workspace, cudaStream_t st) {
   uint16_t* g = reinterpret_cast<uint16_t*>(ws);
   float* part = reinterpret_cast<float*>(ws + p.g_bytes);
   float2* st2 = reinterpret_cast<float2*>(ws + p.g_bytes + p.part_bytes);
-  float* tl = reinterpret_cast<float*>(ws + p.g_bytes + p.part_bytes + p.stats_bytes);
+  uint8_t* rows = ws + p.g_bytes + p.part_bytes + p.stats_bytes;
+  float* tl = reinterpret_cast<float*>(rows);
+  float* factor = reinterpret_cast<float*>(rows + p.row_bytes);
+  float* target_factor = reinterpret_cast<float*>(rows + 2 * p.row_bytes);
+  unsigned* redo = reinterpret_cast<unsigned*>(rows + 3 * p.row_bytes);
   CUtensorMap mWk, mWmn, mPart;
   if (!map_bf16(&mWk, c.W, c.h, c.v, 64, 128) || !map_bf16(&mWmn, c.W, c.h, c.v, 64, 64)) return QLORA_ERR_CUDA;
   if (grad && !make_map_2d(&mPart, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, part, vg::BN, kVocabMaxParts * vg::BM,
@@ -209,7 +213,20 @@ int vocab_core(const VocabCall& c, void* workspace, cudaStream_t st) {
     a.ignore = c.ignore;
     a.stats = st2;
     a.target_logit = tl;
+    a.lse = c.lse + i0;
+    if (grad) {
+      a.dloss = c.dloss + i0;
+      a.dlse = c.dlse ? c.dlse + i0 : nullptr;
+    }
     if (stats) {
+      if (grad) {
+        a.redo = redo;
+        prof::Scope ps(prof::kVocabRows, st);
+        vocab_target_kernel<<<static_cast<unsigned>((n + 7) / 8), 256, 0, st>>>(
+            c.X + i0 * c.h, c.W, a.targets, c.ignore, static_cast<int>(n), static_cast<int>(c.h),
+            static_cast<int>(c.v), tl, redo);
+      }
+      if ((rc = launch_status())) return rc;
       rc = grad ? launch_vocab_gemm<kVocabScaled>(mX, mWk, mGs, mX, a, pairs, st)
                 : launch_vocab_gemm<kVocabStats>(mX, mWk, mX, mX, a, pairs, st);
       if (rc) return rc;
@@ -220,29 +237,31 @@ int vocab_core(const VocabCall& c, void* workspace, cudaStream_t st) {
       r.ignore = c.ignore;
       r.t = static_cast<int>(n);
       r.v = static_cast<int>(c.v);
-      r.n_tiles = a.n_tiles;
+      r.pieces = a.n_tiles;
       r.loss = c.loss + i0;
       r.lse = c.lse + i0;
+      if (grad) {
+        r.dloss = a.dloss;
+        r.factor = factor;
+        r.target_factor = target_factor;
+      }
       {
         prof::Scope ps(prof::kVocabRows, st);
-        if (grad) {
-          r.dloss = c.dloss + i0;
-          r.g = g;
-          r.ldp = a.ldp;
-          vocab_scale_kernel<<<static_cast<unsigned>(n), 256, 0, st>>>(r);
-        } else {
-          vocab_rows_kernel<<<static_cast<unsigned>((n + 7) / 8), 256, 0, st>>>(r);
-        }
+        vocab_rows_kernel<<<static_cast<unsigned>((n + 7) / 8), 256, 0, st>>>(r);
       }
       if ((rc = launch_status())) return rc;
-    } else {
-      a.lse = c.lse + i0;
-      a.dloss = c.dloss + i0;
-      a.dlse = c.dlse ? c.dlse + i0 : nullptr;
-      if ((rc = launch_vocab_gemm<kVocabProb>(mX, mWk, mGs, mX, a, pairs, st))) return rc;
     }
     if (!grad) continue;
-    const VocabGemmArgs d = plan_vocab_gemm(n, c.h, c.v, true, pairs);
+    // g from lse: the backward alone, or again for a run whose scaled exponentials do not serve
+    if ((rc = launch_vocab_gemm<kVocabProb>(mX, mWk, mGs, mX, a, pairs, st))) return rc;
+    VocabGemmArgs d = plan_vocab_gemm(n, c.h, c.v, true, pairs);
+    d.targets = a.targets;
+    d.W = c.W;
+    if (stats) {
+      d.redo = redo;
+      d.factor = factor;
+      d.target_factor = target_factor;
+    }
     if ((rc = launch_vocab_gemm<kVocabGrad>(mG, mWmn, mD, mPart, d, pairs, st))) return rc;
     if (d.splits > 1) {
       const int tiles = d.m_tiles * d.n_tiles - d.whole;

@@ -7,12 +7,24 @@
 // vocab_gemm_kernel is one persistent tcgen05 GEMM with four epilogues. The vocabulary is walked in
 // pieces of 256 columns: a CTA pair computes 256 tokens x 256 columns of logits into tensor memory
 // (fp32) and its epilogue reduces them there:
-//   kVocabStats   a token's maximum and sum of exponentials over the piece (and the target's logit)
-//   kVocabScaled  the same, and exp(l - the piece's maximum) in bf16, for the one-call form
+//   kVocabStats   a token's reference point (its maximum) and sum of exp(l - reference) over the piece,
+//                 and the target's logit
+//   kVocabScaled  the same with the target's logit as the reference, and exp(l - reference) in bf16
 //   kVocabProb    g in bf16, lse being known
 //   kVocabGrad    (the second product, dX = g.W) dX in bf16, or fp32 partial tiles of a split K
 // Only statistics leave the first kernel: 8 bytes per token and piece instead of 512. The backward
 // holds g (or the scaled exponentials) of a bounded run of tokens at a time in the workspace.
+// vocab_narrow_kernel and vocab_narrow_grad_kernel do the same for few tokens, with the operands'
+// roles exchanged.
+//
+// Loss and gradient in one call form the logits once: exp(l - l[y]) needs nothing that is not known
+// when a piece's logits are, floating point keeps its relative precision whatever its scale, and the
+// row's factor dloss.exp(l[y] - lse) is applied to the finished dX. The logits l[y] come first, from a
+// kernel of their own (t dot products). The target's own term is left out of g and added in fp32 as
+// dloss.(exp(-loss) - 1).W[y], so that a confident token's small difference is not one of two rounded
+// numbers. Only where some logit exceeds its row's target by more than 60 (a loss above 60) could the
+// sums overflow: the piece then raises a flag, and kVocabProb runs again over the run with its lse
+// (otherwise that launch returns at once).
 //
 // Bound: the tensor cores (2thv per product) for more than a few hundred tokens, reading W for few.
 // The design follows from the first: cta_group::2 (256 x 256 x 16 per instruction, each CTA loading
@@ -63,6 +75,11 @@ struct VocabGemmArgs {
   const float* lse;      // kVocabProb
   const float* dloss;
   const float* dlse;     // or NULL
+  unsigned* redo;        // kVocabScaled: raised by rows it cannot serve. kVocabProb: NULL, or the flag
+                         // without which there is nothing to do. kVocabGrad: see row_factor
+  const float* factor;   // kVocabGrad: NULL, or a row's factor and its target's
+  const float* target_factor;
+  const uint16_t* W;
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -100,6 +117,50 @@ __device__ __forceinline__ VocabItem vocab_item(const VocabGemmArgs& a, int item
   return it;
 }
 
+// dX from the second product: a row's factor times it, plus its target's factor times W[target].
+// Without factors, or after kVocabProb ran again (g is then complete), the product itself.
+struct RowFactor {
+  float f, ft;
+  const uint16_t* w;   // the target's row of W, or NULL
+  bool plain;
+  // eight columns from `col` on (col < the row's length, a multiple of 8)
+  __device__ __forceinline__ void apply(float (&v)[8], int col) const {
+    if (plain) return;
+    float t[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (w) unpack8(ldg_vec(w, col >> 3), t);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = f == 0.f ? 0.f : fmaf(v[e], f, ft * t[e]);   // not counted: exactly zero
+  }
+};
+__device__ __forceinline__ RowFactor row_factor(const VocabGemmArgs& a, int row) {
+  RowFactor r;
+  r.plain = !a.factor || *a.redo != 0u;
+  r.f = r.ft = 0.f;
+  r.w = nullptr;
+  if (!r.plain && row >= 0) {
+    r.f = a.factor[row];
+    r.ft = a.target_factor[row];
+    if (r.ft != 0.f) r.w = a.W + a.targets[row] * a.N;   // (counted: inside the vocabulary)
+  }
+  return r;
+}
+
+// The reference point of a row's piece whose logits have maximum m: the target's logit c where it
+// serves (kScaled, a counted row), the maximum itself else. An infinite one is no reference point:
+// exp(l) itself then sums to 0 or to infinity (base).
+struct RowRef {
+  float ref, base;
+  bool redo;
+};
+template <bool kScaled>
+__device__ __forceinline__ RowRef row_ref(float m, float c, bool counted) {
+  RowRef r;
+  r.redo = kScaled && counted && m - c > 60.f;
+  r.ref = kScaled && counted && !r.redo ? c : m;
+  r.base = (fabsf(r.ref) == INFINITY ? 0.f : r.ref) * vg::kLog2e;
+  return r;
+}
+
 template <int kMode>
 __global__ void __launch_bounds__(vg::kThreads, 1)
     vocab_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
@@ -119,6 +180,7 @@ __global__ void __launch_bounds__(vg::kThreads, 1)
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drained + 1);
   volatile uint32_t* abort_flag = tmem_holder + 1;
 
+  if (kMode == kVocabProb && args.redo && *args.redo == 0u) return;   // (the whole grid alike)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_ctarank());   // 0: MMA issuer, 1: its peer
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
@@ -260,6 +322,7 @@ __global__ void __launch_bounds__(vg::kThreads, 1)
       };
       if (kMode == kVocabGrad) {
         if (it.part < 0) {
+          const RowFactor rf = row_factor(args, rok ? row : -1);
           for (int c = 0; c < BN; c += 64) {
             uint32_t v[64];
             load64(c, v);
@@ -272,6 +335,7 @@ __global__ void __launch_bounds__(vg::kThreads, 1)
               float f[8];
 #pragma unroll
               for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(v[8 * k + e]);
+              if (it.n0 + c + 8 * k < args.N) rf.apply(f, it.n0 + c + 8 * k);
               *reinterpret_cast<uint4*>(rowp + ((k ^ (lane & 7)) << 4)) = pack8(f);
             }
             end_tile(tile, &tmOut, it.n0 + c, row0, row0 < args.M);
@@ -302,8 +366,9 @@ __global__ void __launch_bounds__(vg::kThreads, 1)
       const bool counted = y >= 0 && y < args.N && y != args.ignore;
       const int tcol = counted && y >= it.n0 && y < it.n0 + BN ? static_cast<int>(y - it.n0) : -1;
       if (kMode == kVocabStats || kMode == kVocabScaled) {
-        // the target's logit, for the few rows whose target lies in this piece
-        for (unsigned left = __ballot_sync(0xFFFFFFFFu, tcol >= 0); left; left &= left - 1) {
+        constexpr bool kScaled = kMode == kVocabScaled;
+        // the target's logit, for the few rows whose target lies in this piece (kVocabScaled has it)
+        for (unsigned left = kScaled ? 0u : __ballot_sync(0xFFFFFFFFu, tcol >= 0); left; left &= left - 1) {
           const int src = __ffs(left) - 1;
           const uint32_t v = tmem_ld_1(taddr + __shfl_sync(0xFFFFFFFFu, tcol, src));
           tmem_ld_wait();
@@ -316,22 +381,24 @@ __global__ void __launch_bounds__(vg::kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 64; ++e) m = fmaxf(m, c + e < vcols ? __uint_as_float(v[e]) : -INFINITY);
         }
-        // an infinite maximum is no reference point: exp(l) itself then sums to 0 or to infinity
-        const float ml = (fabsf(m) == INFINITY ? 0.f : m) * kLog2e;
+        const RowRef rr = row_ref<kScaled>(m, kScaled && counted ? __ldg(args.target_logit + row) : 0.f, counted);
+        if (kScaled && rr.redo) *args.redo = 1u;
         float s0 = 0.f, s1 = 0.f;
         for (int c = 0; c < BN; c += 64) {
-          if (c >= vcols && (kMode == kVocabStats || it.n0 + c >= args.ldp)) break;
+          if (c >= vcols && (!kScaled || it.n0 + c >= args.ldp)) break;
           uint32_t v[64];
           load64(c, v);
           float p[64];
 #pragma unroll
-          for (int e = 0; e < 64; ++e) p[e] = c + e < vcols ? ex2(fmaf(__uint_as_float(v[e]), kLog2e, -ml)) : 0.f;
+          for (int e = 0; e < 64; ++e) p[e] = c + e < vcols ? ex2(fmaf(__uint_as_float(v[e]), kLog2e, -rr.base)) : 0.f;
 #pragma unroll
           for (int e = 0; e < 64; e += 2) {
             s0 += p[e];
             s1 += p[e + 1];
           }
-          if (kMode == kVocabScaled) {
+          if (kScaled) {
+#pragma unroll
+            for (int e = 0; e < 64; ++e) p[e] = c + e == tcol ? 0.f : p[e];
             uint8_t* tile = begin_tile();
             uint8_t* rowp = tile + lane * 128;
 #pragma unroll
@@ -342,7 +409,7 @@ __global__ void __launch_bounds__(vg::kThreads, 1)
           }
         }
         drained_acc();
-        if (rok) args.stats[static_cast<int64_t>(row) * args.n_tiles + it.nt] = make_float2(m, s0 + s1);
+        if (rok) args.stats[static_cast<int64_t>(row) * args.n_tiles + it.nt] = make_float2(rr.ref, s0 + s1);
       } else {
         const float b = counted ? __ldg(args.dloss + row) : 0.f;
         const float a = b + (rok && args.dlse ? __ldg(args.dlse + row) : 0.f);
@@ -385,42 +452,37 @@ __global__ void __launch_bounds__(vg::kThreads, 1)
 // rows
 // ------------------------------------------------------------------------------------------
 struct VocabRowArgs {
-  const float2* stats;        // t x n_tiles
+  const float2* stats;        // t x pieces
   const float* target_logit;
   const int64_t* targets;
   int64_t ignore;
-  int t, v, n_tiles;
+  int t, v, pieces;
   float* loss;
   float* lse;
-  // vocab_scale_kernel only
-  const float* dloss;
-  uint16_t* g;                // t x ldp
-  int ldp;
+  const float* dloss;         // NULL, or: make the rows' factors
+  float* factor;
+  float* target_factor;
 };
 
-// Joins a row's pieces: the larger of two maxima is the new reference point, as in any running
-// softmax. A sum is zero or infinite only where all or some of its logits are infinite.
+// Joins two pieces of a row: the larger reference point is the new one, as in any running softmax. A
+// sum is zero or infinite only where all or some of its logits are infinite.
 __device__ __forceinline__ float2 join_stats(float2 p, float2 q) {
   const float m = fmaxf(p.x, q.x);
   const float r = fabsf(m) == INFINITY ? 0.f : m;
-  // a piece whose maximum is infinite was summed against 0, not against its maximum
+  // a piece whose reference is infinite was summed against 0
   const float pr = fabsf(p.x) == INFINITY ? 0.f : p.x, qr = fabsf(q.x) == INFINITY ? 0.f : q.x;
   const float ps = p.y == 0.f ? 0.f : p.y * ex2((pr - r) * vg::kLog2e);
   const float qs = q.y == 0.f ? 0.f : q.y * ex2((qr - r) * vg::kLog2e);
   return make_float2(m, ps + qs);
 }
 
-// (loss, lse) of a row from its joined statistics.
-__device__ __forceinline__ float2 row_loss(const VocabRowArgs& a, int row, float2 st, bool& counted) {
-  const float lse = (fabsf(st.x) == INFINITY ? 0.f : st.x) + logf(st.y);
-  const int64_t y = a.targets[row];
-  const bool inside = y >= 0 && y < a.v;
-  counted = inside && y != a.ignore;
-  if (!inside && y != a.ignore) report(kDevTarget);
-  return make_float2(counted ? lse - a.target_logit[row] : 0.f, lse);
-}
-
-__device__ __forceinline__ float2 warp_join(float2 st) {
+// A warp per row: loss, lse, and with dloss the factors of dX = factor.(g.W) + target_factor.W[y].
+__global__ void __launch_bounds__(256) vocab_rows_kernel(const VocabRowArgs a) {
+  const int row = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (row >= a.t) return;
+  float2 st = make_float2(-INFINITY, 0.f);
+#pragma unroll 4
+  for (int i = lane; i < a.pieces; i += 32) st = join_stats(st, a.stats[static_cast<int64_t>(row) * a.pieces + i]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     float2 q;
@@ -428,64 +490,43 @@ __device__ __forceinline__ float2 warp_join(float2 st) {
     q.y = __shfl_xor_sync(0xFFFFFFFFu, st.y, o);
     st = join_stats(st, q);
   }
-  return st;
-}
-
-// A warp per row.
-__global__ void __launch_bounds__(256) vocab_rows_kernel(const VocabRowArgs a) {
-  const int row = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (row >= a.t) return;
-  float2 st = make_float2(-INFINITY, 0.f);
-  for (int i = lane; i < a.n_tiles; i += 32) st = join_stats(st, a.stats[static_cast<int64_t>(row) * a.n_tiles + i]);
-  st = warp_join(st);
-  if (lane == 0) {
-    bool counted;
-    const float2 r = row_loss(a, row, st, counted);
-    a.loss[row] = r.x;
-    a.lse[row] = r.y;
-  }
-}
-
-// A CTA per row: the row's loss and lse, then its scaled exponentials become g in place:
-// g_v = dloss . exp(piece's maximum - lse) . (stored exp(l_v - piece's maximum)), and at the target
-// dloss . (exp(l - lse) - 1) from the fp32 logit.
-__global__ void __launch_bounds__(256) vocab_scale_kernel(const VocabRowArgs a) {
-  __shared__ float2 sh[8];
-  __shared__ float s_lse, s_b, s_ty;
-  const int row = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const float2* stats = a.stats + static_cast<int64_t>(row) * a.n_tiles;
-  float2 st = make_float2(-INFINITY, 0.f);
-  for (int i = threadIdx.x; i < a.n_tiles; i += 256) st = join_stats(st, stats[i]);
-  st = warp_join(st);
-  if (lane == 0) sh[warp] = st;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int w = 1; w < 8; ++w) st = join_stats(st, sh[w]);
-    bool counted;
-    const float2 r = row_loss(a, row, st, counted);
-    a.loss[row] = r.x;
-    a.lse[row] = r.y;
-    s_lse = r.y;
-    s_b = counted ? a.dloss[row] : 0.f;
-    s_ty = counted ? s_b * (ex2(-r.x * vg::kLog2e) - 1.f) : 0.f;
-  }
-  __syncthreads();
-  const float lse = s_lse, b = s_b;
+  if (lane != 0) return;
+  const float lse = (fabsf(st.x) == INFINITY ? 0.f : st.x) + logf(st.y);
   const int64_t y = a.targets[row];
-  const int ty = y >= 0 && y < a.v && y != a.ignore ? static_cast<int>(y) : -1;
-  uint4* g = reinterpret_cast<uint4*>(a.g + static_cast<int64_t>(row) * a.ldp);
-  for (int v0 = warp * 32; v0 * 8 < a.ldp; v0 += 256) {   // a warp's 32 vectors of 8: one piece
-    const int v = v0 + lane;
-    if (v * 8 >= a.ldp) continue;
-    float f[8];
-    unpack8(g[v], f);
-    const float m = stats[v0 >> 5].x;
-    const float k = b * ex2(((fabsf(m) == INFINITY ? 0.f : m) - lse) * vg::kLog2e);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = b == 0.f ? 0.f : f[e] * k;
-    if (ty >= 0 && (ty >> 3) == v) f[ty & 7] = s_ty;
-    g[v] = pack8(f);
+  const bool inside = y >= 0 && y < a.v, counted = inside && y != a.ignore;
+  if (!inside && y != a.ignore) report(kDevTarget);
+  const float loss = counted ? lse - a.target_logit[row] : 0.f;
+  a.loss[row] = loss;
+  a.lse[row] = lse;
+  if (a.dloss) {
+    const float d = counted ? a.dloss[row] : 0.f;
+    a.factor[row] = counted ? d * expf(-loss) : 0.f;          // dloss . p[y]
+    a.target_factor[row] = counted ? d * expm1f(-loss) : 0.f;  // dloss . (p[y] - 1)
   }
+}
+
+// The counted rows' target logits, a warp per row, and the redo flag's clearing.
+__global__ void __launch_bounds__(256)
+    vocab_target_kernel(const uint16_t* X, const uint16_t* W, const int64_t* targets, int64_t ignore, int t, int h,
+                        int v, float* target_logit, unsigned* redo) {
+  const int row = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (blockIdx.x == 0 && threadIdx.x == 0) *redo = 0u;
+  if (row >= t) return;
+  const int64_t y = targets[row];
+  if (y < 0 || y >= v || y == ignore) return;
+  const uint16_t *x = X + static_cast<int64_t>(row) * h, *w = W + y * h;
+  float s = 0.f;
+#pragma unroll 4
+  for (int i = lane; i < (h >> 3); i += 32) {
+    float a[8], b[8];
+    unpack8(ldg_vec(x, i), a);
+    unpack8(ldg_vec(w, i), b);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s = fmaf(a[e], b[e], s);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+  if (lane == 0) target_logit[row] = s;
 }
 
 // dX tiles whose K was split: the partial tiles are added in order and rounded once.
@@ -505,6 +546,7 @@ __global__ void __launch_bounds__(256)
     s[0] += u.x; s[1] += u.y; s[2] += u.z; s[3] += u.w;
     s[4] += w.x; s[5] += w.y; s[6] += w.z; s[7] += w.w;
   }
+  row_factor(a, row).apply(s, col);
   *reinterpret_cast<uint4*>(dX + static_cast<int64_t>(row) * a.N + col) = pack8(s);
 }
 
