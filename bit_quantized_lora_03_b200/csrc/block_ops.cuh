@@ -76,21 +76,29 @@ constexpr size_t kVocabRunBytes = size_t(256) << 20;
 constexpr int64_t kVocabMaxV = int64_t(1) << 24;
 constexpr int kVocabMaxParts = kMaxSms;   // partial tiles of a split K
 
+// Up to this many tokens go through the kernels that stream W past them (one 256-token tile of the
+// others is computed whole whatever it holds). Measured on 32000 x 4096: see vocab_loss.cuh.
+constexpr int64_t kVocabNarrowTokens = 128;
+
 struct VocabPlan {
+  bool narrow;
   int64_t run;      // tokens per run
   int64_t ldp;      // v rounded up to 64
   int64_t n_tiles;  // pieces of the vocabulary
   size_t g_bytes, stats_bytes, row_bytes, part_bytes;   // row_bytes: one float per token of a run
 };
-VocabPlan plan_vocab(int64_t t, int64_t v, bool stats, bool grad) {
+VocabPlan plan_vocab(int64_t t, int64_t h, int64_t v, bool stats, bool grad) {
   VocabPlan p{};
+  p.narrow = t <= kVocabNarrowTokens;
   p.ldp = (v + 63) / 64 * 64;
-  p.n_tiles = (v + vg::BN - 1) / vg::BN;
+  p.n_tiles = p.narrow ? p.ldp / vn::kUnit : (v + vg::BN - 1) / vg::BN;
   const int64_t fit = static_cast<int64_t>(kVocabRunBytes / (static_cast<size_t>(p.ldp) * 2));
   p.run = grad ? std::min<int64_t>(t, std::max<int64_t>(vg::BM, fit / vg::BM * vg::BM)) : t;
   if (grad) {
     p.g_bytes = align256(static_cast<size_t>(p.run) * p.ldp * 2);
-    p.part_bytes = static_cast<size_t>(kVocabMaxParts) * vg::BM * vg::BN * 4;
+    p.part_bytes = p.narrow ? static_cast<size_t>(kMaxSms + (h + vn::BM - 1) / vn::BM) * vn::BM *
+                                  vn::tokens16(static_cast<int>(t)) * 4
+                            : static_cast<size_t>(kVocabMaxParts) * vg::BM * vg::BN * 4;
   }
   if (stats) {
     p.stats_bytes = align256(static_cast<size_t>(p.run) * p.n_tiles * 8);
@@ -107,7 +115,7 @@ int check_vocab_shape(int64_t t, int64_t h, int64_t v) {
 
 size_t vocab_ws_bytes(int64_t t, int64_t h, int64_t v, bool stats, bool grad) {
   if (check_vocab_shape(t, h, v) != QLORA_OK) return 0;
-  const VocabPlan p = plan_vocab(t, v, stats, grad);
+  const VocabPlan p = plan_vocab(t, h, v, stats, grad);
   return p.g_bytes + p.part_bytes + p.stats_bytes + 3 * p.row_bytes + 256;
 }
 
@@ -168,6 +176,13 @@ int launch_vocab_gemm(const CUtensorMap& mA, const CUtensorMap& mB, const CUtens
   return launch_status();
 }
 
+template <typename Kernel, typename... Maps>
+int launch_narrow(Kernel kernel, const VocabNarrowArgs& a, int ctas, cudaStream_t st, const Maps&... maps) {
+  prof::Scope ps(prof::kVocabGemm, st);
+  kernel<<<static_cast<unsigned>(ctas), vn::kThreads, vn::smem_bytes(a.n16), st>>>(maps..., a);
+  return launch_status();
+}
+
 struct VocabCall {
   const uint16_t *X, *W;
   int64_t t, h, v;
@@ -185,7 +200,7 @@ int vocab_core(const VocabCall& c, void* workspace, cudaStream_t st) {
   if (sm_count(dev) > kMaxSms) return QLORA_ERR_UNSUPPORTED_DEVICE;
   const int pairs = sm_count(dev) / 2;
   const bool stats = c.loss != nullptr, grad = c.dX != nullptr;
-  const VocabPlan p = plan_vocab(c.t, c.v, stats, grad);
+  const VocabPlan p = plan_vocab(c.t, c.h, c.v, stats, grad);
   uint8_t* ws = reinterpret_cast<uint8_t*>(workspace);
   uint16_t* g = reinterpret_cast<uint16_t*>(ws);
   float* part = reinterpret_cast<float*>(ws + p.g_bytes);
@@ -195,6 +210,89 @@ int vocab_core(const VocabCall& c, void* workspace, cudaStream_t st) {
   float* factor = reinterpret_cast<float*>(rows + p.row_bytes);
   float* target_factor = reinterpret_cast<float*>(rows + 2 * p.row_bytes);
   unsigned* redo = reinterpret_cast<unsigned*>(rows + 3 * p.row_bytes);
+  const auto run_targets = [&](int64_t i0, int64_t n) {
+    prof::Scope ps(prof::kVocabRows, st);
+    vocab_target_kernel<<<static_cast<unsigned>((n + 7) / 8), 256, 0, st>>>(
+        c.X + i0 * c.h, c.W, c.targets + i0, c.ignore, static_cast<int>(n), static_cast<int>(c.h),
+        static_cast<int>(c.v), tl, redo);
+    return launch_status();
+  };
+  const auto run_rows = [&](int64_t i0, int64_t n) {
+    VocabRowArgs r{};
+    r.stats = st2;
+    r.target_logit = tl;
+    r.targets = c.targets + i0;
+    r.ignore = c.ignore;
+    r.t = static_cast<int>(n);
+    r.v = static_cast<int>(c.v);
+    r.pieces = static_cast<int>(p.n_tiles);
+    r.loss = c.loss + i0;
+    r.lse = c.lse + i0;
+    if (grad) {
+      r.dloss = c.dloss + i0;
+      r.factor = factor;
+      r.target_factor = target_factor;
+    }
+    prof::Scope ps(prof::kVocabRows, st);
+    vocab_rows_kernel<<<static_cast<unsigned>((n + 7) / 8), 256, 0, st>>>(r);
+    return launch_status();
+  };
+  if (p.narrow) {
+    VocabNarrowArgs a{};
+    a.t = static_cast<int>(c.t);
+    a.n16 = vn::tokens16(a.t);
+    a.v = static_cast<int>(c.v);
+    a.h = static_cast<int>(c.h);
+    a.num_kb = static_cast<int>((c.h + vn::BK - 1) / vn::BK);
+    a.ldp = static_cast<int>(p.ldp);
+    a.units = a.ldp / vn::kUnit;
+    a.targets = c.targets;
+    a.ignore = c.ignore;
+    a.stats = st2;
+    a.target_logit = tl;
+    a.lse = c.lse;
+    a.dloss = c.dloss;
+    a.dlse = c.dlse;
+    a.redo = stats ? redo : nullptr;
+    a.g = g;
+    a.part = part;
+    CUtensorMap mW, mWu, mX;
+    if (!map_bf16(&mW, c.W, c.h, c.v, 64, vn::BM) || !map_bf16(&mWu, c.W, c.h, c.v, 64, vn::kUnit) ||
+        !map_bf16(&mX, c.X, c.h, c.t, 64, static_cast<uint32_t>(a.n16)))
+      return QLORA_ERR_CUDA;
+    const int ctas = std::min(sm_count(dev), a.units);
+    if (stats) {
+      if (grad && (rc = run_targets(0, c.t))) return rc;
+      if ((rc = grad ? launch_narrow(vocab_narrow_kernel<kVocabScaled>, a, ctas, st, mW, mWu, mX)
+                     : launch_narrow(vocab_narrow_kernel<kVocabStats>, a, ctas, st, mW, mWu, mX)))
+        return rc;
+      if ((rc = run_rows(0, c.t))) return rc;
+    }
+    if (!grad) return QLORA_OK;
+    if ((rc = launch_narrow(vocab_narrow_kernel<kVocabProb>, a, ctas, st, mW, mWu, mX))) return rc;
+    CUtensorMap mWmn, mG;
+    if (!map_bf16(&mWmn, c.W, c.h, c.v, 64, 64) ||
+        !map_bf16(&mG, g, p.ldp, c.t, 64, static_cast<uint32_t>(a.n16)))
+      return QLORA_ERR_CUDA;
+    VocabNarrowArgs d = a;
+    d.num_kb = a.ldp / vn::BK;
+    d.tiles = static_cast<int>((c.h + vn::BM - 1) / vn::BM);
+    const int gctas = static_cast<int>(std::min<int64_t>(sm_count(dev), static_cast<int64_t>(d.tiles) * d.num_kb));
+    if ((rc = launch_narrow(vocab_narrow_grad_kernel, d, gctas, st, mWmn, mG))) return rc;
+    VocabGemmArgs f{};
+    f.N = d.h;
+    f.targets = c.targets;
+    f.W = c.W;
+    if (stats) {
+      f.redo = redo;
+      f.factor = factor;
+      f.target_factor = target_factor;
+    }
+    prof::Scope ps(prof::kVocabRows, st);
+    vocab_narrow_join_kernel<<<dim3(static_cast<unsigned>(d.tiles), static_cast<unsigned>((c.t + 1) / 2)), 256, 0, st>>>(
+        part, c.dX, d, f, gctas);
+    return launch_status();
+  }
   CUtensorMap mWk, mWmn, mPart;
   if (!map_bf16(&mWk, c.W, c.h, c.v, 64, 128) || !map_bf16(&mWmn, c.W, c.h, c.v, 64, 64)) return QLORA_ERR_CUDA;
   if (grad && !make_map_2d(&mPart, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, part, vg::BN, kVocabMaxParts * vg::BM,
@@ -221,35 +319,12 @@ int vocab_core(const VocabCall& c, void* workspace, cudaStream_t st) {
     if (stats) {
       if (grad) {
         a.redo = redo;
-        prof::Scope ps(prof::kVocabRows, st);
-        vocab_target_kernel<<<static_cast<unsigned>((n + 7) / 8), 256, 0, st>>>(
-            c.X + i0 * c.h, c.W, a.targets, c.ignore, static_cast<int>(n), static_cast<int>(c.h),
-            static_cast<int>(c.v), tl, redo);
+        if ((rc = run_targets(i0, n))) return rc;
       }
-      if ((rc = launch_status())) return rc;
       rc = grad ? launch_vocab_gemm<kVocabScaled>(mX, mWk, mGs, mX, a, pairs, st)
                 : launch_vocab_gemm<kVocabStats>(mX, mWk, mX, mX, a, pairs, st);
       if (rc) return rc;
-      VocabRowArgs r{};
-      r.stats = st2;
-      r.target_logit = tl;
-      r.targets = a.targets;
-      r.ignore = c.ignore;
-      r.t = static_cast<int>(n);
-      r.v = static_cast<int>(c.v);
-      r.pieces = a.n_tiles;
-      r.loss = c.loss + i0;
-      r.lse = c.lse + i0;
-      if (grad) {
-        r.dloss = a.dloss;
-        r.factor = factor;
-        r.target_factor = target_factor;
-      }
-      {
-        prof::Scope ps(prof::kVocabRows, st);
-        vocab_rows_kernel<<<static_cast<unsigned>((n + 7) / 8), 256, 0, st>>>(r);
-      }
-      if ((rc = launch_status())) return rc;
+      if ((rc = run_rows(i0, n))) return rc;
     }
     if (!grad) continue;
     // g from lse: the backward alone, or again for a run whose scaled exponentials do not serve

@@ -163,6 +163,11 @@ bool block_ops_attributes() {
                        vocab_gemm_kernel<kVocabProb>, vocab_gemm_kernel<kVocabGrad>})
     fine &= cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  static_cast<int>(vg::smem_bytes())) == cudaSuccess;
+  for (auto* kernel : {vocab_narrow_kernel<kVocabStats>, vocab_narrow_kernel<kVocabScaled>,
+                       vocab_narrow_kernel<kVocabProb>})
+    fine &= cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448) == cudaSuccess;
+  fine &= cudaFuncSetAttribute(vocab_narrow_grad_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448) ==
+          cudaSuccess;
   return fine;
 }
 

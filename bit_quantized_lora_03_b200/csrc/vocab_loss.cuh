@@ -449,6 +449,360 @@ __global__ void __launch_bounds__(vg::kThreads, 1)
 }
 
 // ------------------------------------------------------------------------------------------
+// Few tokens: bound by reading W. The operands change places, D^T = W.X^T, so that an instruction
+// computes 128 words x N tokens with N the tokens rounded up to 16 instead of 256 of them, and the
+// pipeline holds little but W. A CTA takes one contiguous run of the vocabulary in units of 32 words
+// (a warp's rows of an accumulator), which balances the card to a unit whatever the vocabulary;
+// statistics are kept per unit. A warp's lanes are words and its columns tokens: the maximum over a
+// column is one reduction instruction, the sums of 16 columns 16 shuffles.
+// ------------------------------------------------------------------------------------------
+namespace vn {
+constexpr int kMaxTokens = 256;   // one MMA's columns
+constexpr int BM = 128, BK = 64;
+constexpr int kUnit = 32;         // words per unit
+constexpr int A_BYTES = BM * BK * 2;
+constexpr int MAX_STAGES = 10;
+constexpr int kThreads = 6 * 32, kTmaWarp = 4, kMmaWarp = 5;
+constexpr int kTokenBytes = kMaxTokens * 5 * 4;
+constexpr int kRoom = 232448 - 1024 - kTokenBytes - 512;
+__host__ __device__ constexpr int tokens16(int t) { return (t + 15) / 16 * 16; }
+__host__ __device__ constexpr int stage_bytes(int n16) { return A_BYTES + n16 * BK * 2; }
+__host__ __device__ constexpr int stages(int n16) {
+  return kRoom / stage_bytes(n16) < MAX_STAGES ? kRoom / stage_bytes(n16) : MAX_STAGES;
+}
+constexpr size_t smem_bytes(int n16) {
+  return 1024 + static_cast<size_t>(stages(n16)) * stage_bytes(n16) + kTokenBytes + 512;
+}
+}  // namespace vn
+
+struct VocabNarrowArgs {
+  int t, n16;            // tokens, and rounded up to 16
+  int v, h;
+  int num_kb;            // K-steps of 64: of h, or for the gradient of ldp
+  int units;             // ldp / 32
+  int ldp;
+  int tiles;             // the gradient: 128-column tiles of h
+  const int64_t* targets;
+  int64_t ignore;
+  float2* stats;         // t x units
+  float* target_logit;
+  const float* lse;
+  const float* dloss;
+  const float* dlse;
+  unsigned* redo;
+  uint16_t* g;           // t x ldp
+  float* part;           // the gradient's partial tiles: [slot][token][128]
+};
+
+__device__ __forceinline__ float warp_max(float x) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xFFFFFFFF;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// One CTA's shared memory, barriers and tensor memory, the same for both kernels below.
+struct NarrowCta {
+  uint8_t* stage;
+  uint64_t *full, *empty, *acc_full, *acc_empty;
+  uint32_t* tmem_holder;
+  volatile uint32_t* abort_flag;
+  float* token;          // 5 x 256 values per token
+  int stages, stage_bytes;
+  uint32_t tmem_cols, tmem;
+};
+__device__ __forceinline__ NarrowCta narrow_setup(uint8_t* smem_raw, int n16) {
+  NarrowCta c;
+  c.stage = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  c.stages = vn::stages(n16);
+  c.stage_bytes = vn::stage_bytes(n16);
+  c.token = reinterpret_cast<float*>(c.stage + c.stages * c.stage_bytes);
+  c.full = reinterpret_cast<uint64_t*>(c.token + 5 * vn::kMaxTokens);
+  c.empty = c.full + vn::MAX_STAGES;
+  c.acc_full = c.empty + vn::MAX_STAGES;
+  c.acc_empty = c.acc_full + 2;
+  c.tmem_holder = reinterpret_cast<uint32_t*>(c.acc_empty + 2);
+  c.abort_flag = c.tmem_holder + 1;
+  c.tmem_cols = 32;
+  while (c.tmem_cols < 2u * n16) c.tmem_cols *= 2;
+  const int warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < c.stages; ++s) {
+      mbar_init(&c.full[s], 1);
+      mbar_init(&c.empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&c.acc_full[b], 1);
+      mbar_init(&c.acc_empty[b], 4);
+    }
+    *c.abort_flag = 0u;
+    fence_mbar_init();
+  }
+  if (warp == vn::kMmaWarp) {
+    tmem_alloc(c.tmem_holder, c.tmem_cols);
+    tmem_relinquish();
+  }
+  return c;
+}
+__device__ __forceinline__ void narrow_begin(NarrowCta& c) {
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  c.tmem = *c.tmem_holder;
+}
+__device__ __forceinline__ void narrow_end(const NarrowCta& c) {
+  tc_fence_before();
+  __syncthreads();
+  if ((threadIdx.x >> 5) == vn::kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(c.tmem, c.tmem_cols);
+  }
+}
+// A position in the ring: kept by counting, since dividing by a ring size that is known only at run time
+// takes hundreds of cycles, once or more per K-step.
+struct RingPos {
+  int slot = 0;
+  uint32_t phase = 0;
+  int done = 0;          // stages passed
+  __device__ __forceinline__ void next(int stages) {
+    ++done;
+    if (++slot == stages) {
+      slot = 0;
+      phase ^= 1u;
+    }
+  }
+};
+// The MMA thread's part of one accumulator: `steps` K-steps from the ring at position g.
+template <bool kAmn>
+__device__ __forceinline__ bool narrow_mma(const NarrowCta& c, int n16, int buf, int n, int steps, RingPos& g) {
+  if (!mbar_wait(&c.acc_empty[buf], ((n >> 1) & 1) ^ 1u, c.abort_flag)) return false;
+  tc_fence_after();
+  const uint32_t idesc = idesc_bf16(vn::BM, n16, kAmn, false);
+  for (int k = 0; k < steps; ++k, g.next(c.stages)) {
+    const int slot = g.slot;
+    if (!mbar_wait(&c.full[slot], g.phase, c.abort_flag)) return false;
+    tc_fence_after();
+    const uint32_t a_addr = smem_addr(c.stage + slot * c.stage_bytes), b_addr = a_addr + vn::A_BYTES;
+#pragma unroll
+    for (int kk = 0; kk < vn::BK / 16; ++kk)
+      umma_bf16(c.tmem + buf * (c.tmem_cols / 2),
+                kAmn ? sw128_desc(a_addr + kk * 2048, 8192, 1024) : sw128_desc(a_addr + kk * 32, 16, 1024),
+                sw128_desc(b_addr + kk * 32, 16, 1024), idesc, (k > 0 || kk > 0) ? 1u : 0u);
+    umma_commit(&c.empty[slot]);
+  }
+  umma_commit(&c.acc_full[buf]);
+  return true;
+}
+// After an abort: no copy may still be writing shared memory, no MMA reading it, when the CTA exits.
+__device__ __forceinline__ void narrow_drain_copies(const NarrowCta& c, const RingPos& g) {
+  if (*c.abort_flag)
+    for (int j = (g.done > c.stages ? g.done - c.stages : 0); j < g.done; ++j)
+      mbar_drain(&c.full[j % c.stages], (j / c.stages) & 1);
+}
+__device__ __forceinline__ void narrow_drain_mma(const NarrowCta& c, const RingPos& g) {
+  // (each stage's commit arrives on its `empty` barrier and covers all MMAs before it)
+  if (*c.abort_flag && g.done > 0) mbar_drain(&c.empty[(g.done - 1) % c.stages], ((g.done - 1) / c.stages) & 1);
+}
+
+template <int kMode>
+__global__ void __launch_bounds__(vn::kThreads, 1)
+    vocab_narrow_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmWu,
+                        const __grid_constant__ CUtensorMap tmX, const VocabNarrowArgs args) {
+  using namespace vn;
+  extern __shared__ uint8_t smem_raw[];
+  if (kMode == kVocabProb && args.redo && *args.redo == 0u) return;   // (the whole grid alike)
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  NarrowCta cta = narrow_setup(smem_raw, args.n16);
+  // per token: what the epilogue needs of it (a word that is nobody's target: -1)
+  float *t_ref = cta.token, *t_a = cta.token + kMaxTokens, *t_b = cta.token + 2 * kMaxTokens;
+  int* t_word = reinterpret_cast<int*>(cta.token + 3 * kMaxTokens);
+  for (int n = threadIdx.x; n < args.n16; n += kThreads) {
+    const int64_t y = n < args.t ? args.targets[n] : -1;
+    const bool counted = y >= 0 && y < args.v && y != args.ignore;
+    t_word[n] = counted ? static_cast<int>(y) : -1;
+    if (kMode == kVocabScaled) t_ref[n] = counted ? args.target_logit[n] : 0.f;
+    if (kMode == kVocabProb) {
+      const float b = counted ? args.dloss[n] : 0.f;
+      t_b[n] = b;
+      t_a[n] = b + (n < args.t && args.dlse ? args.dlse[n] : 0.f);
+      t_ref[n] = n < args.t ? -args.lse[n] * vg::kLog2e : 0.f;
+    }
+  }
+  narrow_begin(cta);
+  const int u0 = unit_row(args.units, gridDim.x, blockIdx.x), u1 = unit_row(args.units, gridDim.x, blockIdx.x + 1);
+
+  if (warp == kTmaWarp) {
+    if (lane == 0) {
+      RingPos g;
+      bool ok = true;
+      for (int u = u0; ok && u < u1; u += 4) {
+        const int nu = min(4, u1 - u);
+        for (int kb = 0; kb < args.num_kb; ++kb, g.next(cta.stages)) {
+          const int slot = g.slot;
+          if (!mbar_wait(&cta.empty[slot], g.phase ^ 1u, cta.abort_flag)) { ok = false; break; }
+          uint8_t* dst = cta.stage + slot * cta.stage_bytes;
+          mbar_arrive_expect_tx(&cta.full[slot], nu * (kUnit * BK * 2) + args.n16 * (BK * 2));
+          if (nu == 4) {   // (one copy of 128 rows: four of 32 take longer)
+            tma_load_2d(dst, &tmW, &cta.full[slot], kb * BK, u * kUnit);
+          } else {
+            for (int i = 0; i < nu; ++i)
+              tma_load_2d(dst + i * (kUnit * BK * 2), &tmWu, &cta.full[slot], kb * BK, (u + i) * kUnit);
+          }
+          tma_load_2d(dst + A_BYTES, &tmX, &cta.full[slot], kb * BK, 0);
+        }
+      }
+      narrow_drain_copies(cta, g);
+    }
+  } else if (warp == kMmaWarp) {
+    if (lane == 0) {
+      RingPos g;
+      int n = 0;
+      // (a last tile of fewer than four units leaves the other rows of its operand as they were: their
+      // accumulator rows are not read)
+      for (int u = u0; u < u1; u += 4, ++n)
+        if (!narrow_mma<false>(cta, args.n16, n & 1, n, args.num_kb, g)) break;
+      narrow_drain_mma(cta, g);
+    }
+  } else {
+    int n = 0;
+    for (int u = u0; u < u1; u += 4, ++n) {
+      const int buf = n & 1;
+      if (!mbar_wait_warp(&cta.acc_full[buf], (n >> 1) & 1, cta.abort_flag)) break;
+      tc_fence_after();
+      const int unit = u + warp;
+      if (unit < u1) {
+        const uint32_t taddr = cta.tmem + (static_cast<uint32_t>(warp * 32) << 16) + buf * (cta.tmem_cols / 2);
+        const int word = unit * kUnit + lane;
+        const bool wok = word < args.v;
+        for (int c = 0; c < args.n16; c += 16) {
+          uint32_t v[16];
+          tmem_ld_16(taddr + c, v);
+          tmem_ld_wait();
+          float p[16];
+          if (kMode == kVocabProb) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const float a = t_a[c + j];
+              // a row that counts for nothing is zero whatever its logits are
+              p[j] = wok && a != 0.f ? a * ex2(fmaf(__uint_as_float(v[j]), vg::kLog2e, t_ref[c + j])) : 0.f;
+              if (word == t_word[c + j]) p[j] -= t_b[c + j];
+            }
+          } else {
+            constexpr bool kScaled = kMode == kVocabScaled;
+            float mine = 0.f;    // the reference of this lane's token (lane / 2) below
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const float l = wok ? __uint_as_float(v[j]) : -INFINITY;
+              const int w = t_word[c + j];
+              const RowRef rr = row_ref<kScaled>(warp_max(l), kScaled ? t_ref[c + j] : 0.f, w >= 0);
+              if (kScaled && rr.redo && lane == 0) *args.redo = 1u;
+              if (!kScaled && word == w) args.target_logit[c + j] = l;
+              if ((lane >> 1) == j) mine = rr.ref;
+              p[j] = wok ? ex2(fmaf(l, vg::kLog2e, -rr.base)) : 0.f;
+            }
+            float q[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) q[j] = p[j];
+            // sums of 16 columns over the lanes: each exchange halves the columns a lane holds
+#pragma unroll
+            for (int o = 16; o > 1; o >>= 1) {
+#pragma unroll
+              for (int j = 0; j < o / 2; ++j) {
+                const float keep = (lane & o) ? q[j + o / 2] : q[j], give = (lane & o) ? q[j] : q[j + o / 2];
+                q[j] = keep + __shfl_xor_sync(0xFFFFFFFFu, give, o);
+              }
+            }
+            q[0] += __shfl_xor_sync(0xFFFFFFFFu, q[0], 1);
+            const int tok = c + (lane >> 1);
+            if (!(lane & 1) && tok < args.t)
+              args.stats[static_cast<int64_t>(tok) * args.units + unit] = make_float2(mine, q[0]);
+            if (kScaled) {
+#pragma unroll
+              for (int j = 0; j < 16; ++j) p[j] = word == t_word[c + j] ? 0.f : p[j];
+            }
+          }
+          if (kMode != kVocabStats) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)   // a token's 32 words: 64 contiguous bytes
+              if (c + j < args.t)
+                args.g[static_cast<int64_t>(c + j) * args.ldp + word] = __bfloat16_as_ushort(__float2bfloat16_rn(p[j]));
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&cta.acc_empty[buf]);
+    }
+  }
+  narrow_end(cta);
+}
+
+// The second product for few tokens, dX^T = W^T.g^T: the K-steps of all 128-column tiles of h in one
+// line, an equal contiguous run of them to each CTA, whose share of a tile goes to a partial tile of
+// its own (number CTA + tile); vocab_narrow_join_kernel adds a tile's shares in order.
+__global__ void __launch_bounds__(vn::kThreads, 1)
+    vocab_narrow_grad_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmG,
+                             const VocabNarrowArgs args) {
+  using namespace vn;
+  extern __shared__ uint8_t smem_raw[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  NarrowCta cta = narrow_setup(smem_raw, args.n16);
+  narrow_begin(cta);
+  const int total = args.tiles * args.num_kb;
+  const int x0 = unit_row(total, gridDim.x, blockIdx.x), x1 = unit_row(total, gridDim.x, blockIdx.x + 1);
+  auto share_end = [&](int x) { return min(x1, (x / args.num_kb + 1) * args.num_kb); };
+
+  if (warp == kTmaWarp) {
+    if (lane == 0) {
+      RingPos g;
+      int tile = x0 / args.num_kb, kb = x0 - tile * args.num_kb;
+      for (int x = x0; x < x1; ++x, g.next(cta.stages)) {
+        const int slot = g.slot;
+        if (!mbar_wait(&cta.empty[slot], g.phase ^ 1u, cta.abort_flag)) break;
+        uint8_t* dst = cta.stage + slot * cta.stage_bytes;
+        mbar_arrive_expect_tx(&cta.full[slot], A_BYTES + args.n16 * (BK * 2));
+        tma_load_2d(dst, &tmW, &cta.full[slot], tile * BM, kb * BK);
+        tma_load_2d(dst + 8192, &tmW, &cta.full[slot], tile * BM + 64, kb * BK);
+        tma_load_2d(dst + A_BYTES, &tmG, &cta.full[slot], kb * BK, 0);
+        if (++kb == args.num_kb) {
+          kb = 0;
+          ++tile;
+        }
+      }
+      narrow_drain_copies(cta, g);
+    }
+  } else if (warp == kMmaWarp) {
+    if (lane == 0) {
+      RingPos g;
+      int n = 0;
+      for (int x = x0; x < x1; x = share_end(x), ++n)
+        if (!narrow_mma<true>(cta, args.n16, n & 1, n, share_end(x) - x, g)) break;
+      narrow_drain_mma(cta, g);
+    }
+  } else {
+    int n = 0;
+    for (int x = x0; x < x1; x = share_end(x), ++n) {
+      const int buf = n & 1;
+      if (!mbar_wait_warp(&cta.acc_full[buf], (n >> 1) & 1, cta.abort_flag)) break;
+      tc_fence_after();
+      const uint32_t taddr = cta.tmem + (static_cast<uint32_t>(warp * 32) << 16) + buf * (cta.tmem_cols / 2);
+      float* dst = args.part + static_cast<int64_t>(blockIdx.x + x / args.num_kb) * args.n16 * BM + warp * 32 + lane;
+      for (int c = 0; c < args.n16; c += 16) {
+        uint32_t v[16];
+        tmem_ld_16(taddr + c, v);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+          if (c + j < args.t) dst[static_cast<int64_t>(c + j) * BM] = __uint_as_float(v[j]);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&cta.acc_empty[buf]);
+    }
+  }
+  narrow_end(cta);
+}
+
+// ------------------------------------------------------------------------------------------
 // rows
 // ------------------------------------------------------------------------------------------
 struct VocabRowArgs {
@@ -548,6 +902,27 @@ __global__ void __launch_bounds__(256)
   }
   row_factor(a, row).apply(s, col);
   *reinterpret_cast<uint4*>(dX + static_cast<int64_t>(row) * a.N + col) = pack8(s);
+}
+
+// The same for few tokens: grid x a 128-column tile of h, grid y two tokens.
+__global__ void __launch_bounds__(256)
+    vocab_narrow_join_kernel(const float* part, uint16_t* dX, const VocabNarrowArgs a, const VocabGemmArgs f, int ctas) {
+  const int tile = blockIdx.x, col = threadIdx.x & 127, tok = blockIdx.y * 2 + (threadIdx.x >> 7);
+  if (tok >= a.t || tile * vn::BM + col >= a.h) return;
+  const int total = a.tiles * a.num_kb, base = total / ctas, extra = total - base * ctas;
+  auto cta_of = [&](int x) {   // the CTA whose run has K-step x (the inverse of unit_row)
+    const int long_runs = extra * (base + 1);
+    return x < long_runs ? x / (base + 1) : extra + (x - long_runs) / base;
+  };
+  const int first = cta_of(tile * a.num_kb), last = cta_of((tile + 1) * a.num_kb - 1);
+  float s = 0.f;
+#pragma unroll 4
+  for (int i = first; i <= last; ++i)
+    s += __ldcg(part + (static_cast<int64_t>(i + tile) * a.n16 + tok) * vn::BM + col);
+  const RowFactor rf = row_factor(f, tok);
+  const int hc = tile * vn::BM + col;
+  if (!rf.plain) s = rf.f == 0.f ? 0.f : fmaf(s, rf.f, rf.w ? rf.ft * bf16_bits_to_float(rf.w[hc]) : 0.f);
+  dX[static_cast<int64_t>(tok) * a.h + hc] = __bfloat16_as_ushort(__float2bfloat16_rn(s));
 }
 
 }  // namespace qlora
