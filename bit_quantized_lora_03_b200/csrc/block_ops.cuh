@@ -77,8 +77,10 @@ constexpr int64_t kVocabMaxV = int64_t(1) << 24;
 constexpr int kVocabMaxParts = kMaxSms;   // partial tiles of a split K
 
 // Up to this many tokens go through the kernels that stream W past them (one 256-token tile of the
-// others is computed whole whatever it holds). Measured on 32000 x 4096: see vocab_loss.cuh.
-constexpr int64_t kVocabNarrowTokens = 128;
+// others is computed whole whatever it holds). Measured on 32000 x 4096, loss and
+// gradient: 104 us at 16 tokens, 111 at 64, 125 at 128, against 123 for any number up to 256.
+constexpr int64_t kVocabNarrowTokens = 112;
+constexpr int64_t kFewRows = 1024;   // rows that get a CTA each in the kernels over rows (a warp each above)
 
 struct VocabPlan {
   bool narrow;
@@ -127,7 +129,7 @@ VocabGemmArgs plan_vocab_gemm(int64_t M, int64_t N, int64_t K, bool split, int p
   VocabGemmArgs a{};
   a.M = static_cast<int>(M);
   a.N = static_cast<int>(N);
-  a.num_kb = static_cast<int>((K + vg::BK - 1) / vg::BK);
+  a.num_kb = static_cast<int>((K + vg::KS * vg::BK - 1) / (vg::KS * vg::BK));
   a.m_tiles = static_cast<int>((M + vg::BM - 1) / vg::BM);
   a.n_tiles = static_cast<int>((N + vg::BN - 1) / vg::BN);
   a.m_group = std::min(a.m_tiles, 16);
@@ -135,7 +137,7 @@ VocabGemmArgs plan_vocab_gemm(int64_t M, int64_t N, int64_t K, bool split, int p
   const int rest = static_cast<int>(tiles % pairs);
   a.splits = 1;
   double best = 1.0;
-  for (int s = 2; split && rest && rest * s <= kVocabMaxParts && s <= a.num_kb / 4; ++s) {
+  for (int s = 2; split && rest && rest * s <= kVocabMaxParts && s <= a.num_kb / 2; ++s) {
     const double cost = static_cast<double>((rest * s + pairs - 1) / pairs) / s + 0.01 * s;
     if (cost < best) {
       best = cost;
@@ -212,7 +214,8 @@ int vocab_core(const VocabCall& c, void* workspace, cudaStream_t st) {
   unsigned* redo = reinterpret_cast<unsigned*>(rows + 3 * p.row_bytes);
   const auto run_targets = [&](int64_t i0, int64_t n) {
     prof::Scope ps(prof::kVocabRows, st);
-    vocab_target_kernel<<<static_cast<unsigned>((n + 7) / 8), 256, 0, st>>>(
+    const bool few = n <= kFewRows;
+    (few ? vocab_target_kernel<8> : vocab_target_kernel<1>)<<<static_cast<unsigned>(few ? n : (n + 7) / 8), 256, 0, st>>>(
         c.X + i0 * c.h, c.W, c.targets + i0, c.ignore, static_cast<int>(n), static_cast<int>(c.h),
         static_cast<int>(c.v), tl, redo);
     return launch_status();
@@ -234,7 +237,8 @@ int vocab_core(const VocabCall& c, void* workspace, cudaStream_t st) {
       r.target_factor = target_factor;
     }
     prof::Scope ps(prof::kVocabRows, st);
-    vocab_rows_kernel<<<static_cast<unsigned>((n + 7) / 8), 256, 0, st>>>(r);
+    const bool few = n <= kFewRows;
+    (few ? vocab_rows_kernel<8> : vocab_rows_kernel<1>)<<<static_cast<unsigned>(few ? n : (n + 7) / 8), 256, 0, st>>>(r);
     return launch_status();
   };
   if (p.narrow) {
@@ -243,7 +247,7 @@ int vocab_core(const VocabCall& c, void* workspace, cudaStream_t st) {
     a.n16 = vn::tokens16(a.t);
     a.v = static_cast<int>(c.v);
     a.h = static_cast<int>(c.h);
-    a.num_kb = static_cast<int>((c.h + vn::BK - 1) / vn::BK);
+    a.num_kb = static_cast<int>((c.h + vn::KS * vn::BK - 1) / (vn::KS * vn::BK));
     a.ldp = static_cast<int>(p.ldp);
     a.units = a.ldp / vn::kUnit;
     a.targets = c.targets;
@@ -275,7 +279,7 @@ int vocab_core(const VocabCall& c, void* workspace, cudaStream_t st) {
         !map_bf16(&mG, g, p.ldp, c.t, 64, static_cast<uint32_t>(a.n16)))
       return QLORA_ERR_CUDA;
     VocabNarrowArgs d = a;
-    d.num_kb = a.ldp / vn::BK;
+    d.num_kb = (a.ldp + vn::KS * vn::BK - 1) / (vn::KS * vn::BK);
     d.tiles = static_cast<int>((c.h + vn::BM - 1) / vn::BM);
     const int gctas = static_cast<int>(std::min<int64_t>(sm_count(dev), static_cast<int64_t>(d.tiles) * d.num_kb));
     if ((rc = launch_narrow(vocab_narrow_grad_kernel, d, gctas, st, mWmn, mG))) return rc;

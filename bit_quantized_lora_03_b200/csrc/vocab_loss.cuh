@@ -42,10 +42,11 @@ namespace qlora {
 
 namespace vg {
 constexpr int BM = 256, BN = 256, BK = 64;   // per CTA pair
-constexpr int STAGES = 6;
-constexpr int A_BYTES = 128 * BK * 2;        // this CTA's half of A
-constexpr int B_BYTES = 128 * BK * 2;        // and of B
-constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
+constexpr int KS = 2;                        // K-steps of 64 per stage
+constexpr int STAGES = 3;
+constexpr int ATOM = 128 * BK * 2;           // this CTA's half of A, or of B, for one step
+constexpr int A_BYTES = KS * ATOM;
+constexpr int STAGE_BYTES = 2 * A_BYTES;
 constexpr int kEpiWarps = 4;
 constexpr int kTmaWarp = 4, kMmaWarp = 5;
 constexpr int kThreads = 6 * 32;
@@ -61,7 +62,7 @@ enum VocabMode : int { kVocabStats = 0, kVocabScaled = 1, kVocabProb = 2, kVocab
 
 struct VocabGemmArgs {
   int M, N;              // rows and columns of the product (N: v, or h for kVocabGrad)
-  int num_kb;            // K-steps of 64
+  int num_kb;            // stages of 128 along K
   int m_tiles, n_tiles;
   int m_group;           // row tiles that are walked together, column tile by column tile
   int whole;             // tiles computed in one piece; the ones behind are split along K
@@ -228,12 +229,17 @@ __global__ void __launch_bounds__(vg::kThreads, 1)
           uint8_t* dst = smem + slot * STAGE_BYTES;
           if (rank == 0) mbar_arrive_expect_tx(&full[slot], 2 * STAGE_BYTES);
           const uint32_t bar = full0 + static_cast<uint32_t>(slot * sizeof(uint64_t));
-          tma_load_2d_pair(dst, &tmA, bar, kb * BK, it.m0 + rank * 128);
-          if (!kBmn) {
-            tma_load_2d_pair(dst + A_BYTES, &tmB, bar, kb * BK, it.n0 + rank * 128);
-          } else {
-            tma_load_2d_pair(dst + A_BYTES, &tmB, bar, it.n0 + rank * 128, kb * BK);
-            tma_load_2d_pair(dst + A_BYTES + 8192, &tmB, bar, it.n0 + rank * 128 + 64, kb * BK);
+#pragma unroll
+          for (int s = 0; s < KS; ++s) {   // (a step behind K's end is filled with zeros)
+            const int k = (kb * KS + s) * BK;
+            uint8_t *a_dst = dst + s * ATOM, *b_dst = dst + A_BYTES + s * ATOM;
+            tma_load_2d_pair(a_dst, &tmA, bar, k, it.m0 + rank * 128);
+            if (!kBmn) {
+              tma_load_2d_pair(b_dst, &tmB, bar, k, it.n0 + rank * 128);
+            } else {
+              tma_load_2d_pair(b_dst, &tmB, bar, it.n0 + rank * 128, k);
+              tma_load_2d_pair(b_dst + 8192, &tmB, bar, it.n0 + rank * 128 + 64, k);
+            }
           }
         }
       }
@@ -262,13 +268,16 @@ __global__ void __launch_bounds__(vg::kThreads, 1)
           const uint32_t ph = (g / STAGES) & 1;
           if (!mbar_wait(&full[slot], ph, abort_flag)) { ok = false; break; }
           tc_fence_after();
-          const uint32_t a_addr = smem_addr(smem + slot * STAGE_BYTES), b_addr = a_addr + A_BYTES;
 #pragma unroll
-          for (int kk = 0; kk < BK / 16; ++kk) {
-            const uint64_t ad = sw128_desc(a_addr + kk * 32, 16, 1024);
-            const uint64_t bd = kBmn ? sw128_desc(b_addr + kk * 2048, 8192, 1024)
-                                     : sw128_desc(b_addr + kk * 32, 16, 1024);
-            umma2_bf16(tmem_base + buf * BN, ad, bd, kIdesc, (kb > it.kb0 || kk > 0) ? 1u : 0u);
+          for (int s = 0; s < KS; ++s) {
+            const uint32_t a_addr = smem_addr(smem + slot * STAGE_BYTES) + s * ATOM, b_addr = a_addr + A_BYTES;
+#pragma unroll
+            for (int kk = 0; kk < BK / 16; ++kk) {
+              const uint64_t ad = sw128_desc(a_addr + kk * 32, 16, 1024);
+              const uint64_t bd = kBmn ? sw128_desc(b_addr + kk * 2048, 8192, 1024)
+                                       : sw128_desc(b_addr + kk * 32, 16, 1024);
+              umma2_bf16(tmem_base + buf * BN, ad, bd, kIdesc, (kb > it.kb0 || s > 0 || kk > 0) ? 1u : 0u);
+            }
           }
           umma2_commit_multicast(&empty[slot], 0x3);   // frees the stage in both CTAs
         }
@@ -459,14 +468,17 @@ __global__ void __launch_bounds__(vg::kThreads, 1)
 namespace vn {
 constexpr int kMaxTokens = 256;   // one MMA's columns
 constexpr int BM = 128, BK = 64;
+constexpr int KS = 2;             // K-steps of 64 per stage: a stage's waits and copies cost some 700 cycles
+                                  // whatever it holds, so that 16 KB of W each were not enough to keep up with HBM
 constexpr int kUnit = 32;         // words per unit
-constexpr int A_BYTES = BM * BK * 2;
-constexpr int MAX_STAGES = 10;
+constexpr int A_ATOM = BM * BK * 2;      // 128 words (or columns of h) x 64 K
+constexpr int A_BYTES = KS * A_ATOM;
+constexpr int MAX_STAGES = 6;
 constexpr int kThreads = 6 * 32, kTmaWarp = 4, kMmaWarp = 5;
 constexpr int kTokenBytes = kMaxTokens * 5 * 4;
 constexpr int kRoom = 232448 - 1024 - kTokenBytes - 512;
 __host__ __device__ constexpr int tokens16(int t) { return (t + 15) / 16 * 16; }
-__host__ __device__ constexpr int stage_bytes(int n16) { return A_BYTES + n16 * BK * 2; }
+__host__ __device__ constexpr int stage_bytes(int n16) { return A_BYTES + KS * n16 * BK * 2; }
 __host__ __device__ constexpr int stages(int n16) {
   return kRoom / stage_bytes(n16) < MAX_STAGES ? kRoom / stage_bytes(n16) : MAX_STAGES;
 }
@@ -478,7 +490,7 @@ constexpr size_t smem_bytes(int n16) {
 struct VocabNarrowArgs {
   int t, n16;            // tokens, and rounded up to 16
   int v, h;
-  int num_kb;            // K-steps of 64: of h, or for the gradient of ldp
+  int num_kb;            // stages of 128 along K: of h, or for the gradient of ldp
   int units;             // ldp / 32
   int ldp;
   int tiles;             // the gradient: 128-column tiles of h
@@ -581,12 +593,16 @@ __device__ __forceinline__ bool narrow_mma(const NarrowCta& c, int n16, int buf,
     const int slot = g.slot;
     if (!mbar_wait(&c.full[slot], g.phase, c.abort_flag)) return false;
     tc_fence_after();
-    const uint32_t a_addr = smem_addr(c.stage + slot * c.stage_bytes), b_addr = a_addr + vn::A_BYTES;
 #pragma unroll
-    for (int kk = 0; kk < vn::BK / 16; ++kk)
-      umma_bf16(c.tmem + buf * (c.tmem_cols / 2),
-                kAmn ? sw128_desc(a_addr + kk * 2048, 8192, 1024) : sw128_desc(a_addr + kk * 32, 16, 1024),
-                sw128_desc(b_addr + kk * 32, 16, 1024), idesc, (k > 0 || kk > 0) ? 1u : 0u);
+    for (int s = 0; s < vn::KS; ++s) {
+      const uint32_t a_addr = smem_addr(c.stage + slot * c.stage_bytes) + s * vn::A_ATOM;
+      const uint32_t b_addr = smem_addr(c.stage + slot * c.stage_bytes) + vn::A_BYTES + s * n16 * (vn::BK * 2);
+#pragma unroll
+      for (int kk = 0; kk < vn::BK / 16; ++kk)
+        umma_bf16(c.tmem + buf * (c.tmem_cols / 2),
+                  kAmn ? sw128_desc(a_addr + kk * 2048, 8192, 1024) : sw128_desc(a_addr + kk * 32, 16, 1024),
+                  sw128_desc(b_addr + kk * 32, 16, 1024), idesc, (k > 0 || s > 0 || kk > 0) ? 1u : 0u);
+    }
     umma_commit(&c.empty[slot]);
   }
   umma_commit(&c.acc_full[buf]);
@@ -640,14 +656,18 @@ __global__ void __launch_bounds__(vn::kThreads, 1)
           const int slot = g.slot;
           if (!mbar_wait(&cta.empty[slot], g.phase ^ 1u, cta.abort_flag)) { ok = false; break; }
           uint8_t* dst = cta.stage + slot * cta.stage_bytes;
-          mbar_arrive_expect_tx(&cta.full[slot], nu * (kUnit * BK * 2) + args.n16 * (BK * 2));
-          if (nu == 4) {   // (one copy of 128 rows: four of 32 take longer)
-            tma_load_2d(dst, &tmW, &cta.full[slot], kb * BK, u * kUnit);
-          } else {
-            for (int i = 0; i < nu; ++i)
-              tma_load_2d(dst + i * (kUnit * BK * 2), &tmWu, &cta.full[slot], kb * BK, (u + i) * kUnit);
+          mbar_arrive_expect_tx(&cta.full[slot], KS * (nu * (kUnit * BK * 2) + args.n16 * (BK * 2)));
+#pragma unroll
+          for (int s = 0; s < KS; ++s) {   // (a step behind h is filled with zeros)
+            const int x = (kb * KS + s) * BK;
+            if (nu == 4) {   // (one copy of 128 rows: four of 32 take longer)
+              tma_load_2d(dst + s * A_ATOM, &tmW, &cta.full[slot], x, u * kUnit);
+            } else {
+              for (int i = 0; i < nu; ++i)
+                tma_load_2d(dst + s * A_ATOM + i * (kUnit * BK * 2), &tmWu, &cta.full[slot], x, (u + i) * kUnit);
+            }
+            tma_load_2d(dst + A_BYTES + s * args.n16 * (BK * 2), &tmX, &cta.full[slot], x, 0);
           }
-          tma_load_2d(dst + A_BYTES, &tmX, &cta.full[slot], kb * BK, 0);
         }
       }
       narrow_drain_copies(cta, g);
@@ -759,10 +779,14 @@ __global__ void __launch_bounds__(vn::kThreads, 1)
         const int slot = g.slot;
         if (!mbar_wait(&cta.empty[slot], g.phase ^ 1u, cta.abort_flag)) break;
         uint8_t* dst = cta.stage + slot * cta.stage_bytes;
-        mbar_arrive_expect_tx(&cta.full[slot], A_BYTES + args.n16 * (BK * 2));
-        tma_load_2d(dst, &tmW, &cta.full[slot], tile * BM, kb * BK);
-        tma_load_2d(dst + 8192, &tmW, &cta.full[slot], tile * BM + 64, kb * BK);
-        tma_load_2d(dst + A_BYTES, &tmG, &cta.full[slot], kb * BK, 0);
+        mbar_arrive_expect_tx(&cta.full[slot], cta.stage_bytes);
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {   // (a step behind ldp is filled with zeros)
+          const int k = (kb * KS + s) * BK;
+          tma_load_2d(dst + s * A_ATOM, &tmW, &cta.full[slot], tile * BM, k);
+          tma_load_2d(dst + s * A_ATOM + 8192, &tmW, &cta.full[slot], tile * BM + 64, k);
+          tma_load_2d(dst + A_BYTES + s * args.n16 * (BK * 2), &tmG, &cta.full[slot], k, 0);
+        }
         if (++kb == args.num_kb) {
           kb = 0;
           ++tile;
@@ -830,13 +854,17 @@ __device__ __forceinline__ float2 join_stats(float2 p, float2 q) {
   return make_float2(m, ps + qs);
 }
 
-// A warp per row: loss, lse, and with dloss the factors of dX = factor.(g.W) + target_factor.W[y].
+// Loss, lse, and with dloss the factors of dX = factor.(g.W) + target_factor.W[y]. kWarps: a row's
+// warps: one, or all eight of a CTA where there are few rows (its pieces then come in one go).
+template <int kWarps>
 __global__ void __launch_bounds__(256) vocab_rows_kernel(const VocabRowArgs a) {
-  const int row = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (row >= a.t) return;
+  __shared__ float2 sh[8];
+  const int row = blockIdx.x * (8 / kWarps) + (threadIdx.x >> 5) / kWarps, lane = threadIdx.x & 31;
+  if (row >= a.t) return;   // (whole warps; with eight to a row no CTA is without one)
   float2 st = make_float2(-INFINITY, 0.f);
 #pragma unroll 4
-  for (int i = lane; i < a.pieces; i += 32) st = join_stats(st, a.stats[static_cast<int64_t>(row) * a.pieces + i]);
+  for (int i = threadIdx.x % (32 * kWarps); i < a.pieces; i += 32 * kWarps)
+    st = join_stats(st, a.stats[static_cast<int64_t>(row) * a.pieces + i]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     float2 q;
@@ -844,7 +872,13 @@ __global__ void __launch_bounds__(256) vocab_rows_kernel(const VocabRowArgs a) {
     q.y = __shfl_xor_sync(0xFFFFFFFFu, st.y, o);
     st = join_stats(st, q);
   }
-  if (lane != 0) return;
+  if (kWarps > 1) {
+    if (lane == 0) sh[threadIdx.x >> 5] = st;
+    __syncthreads();
+    if (threadIdx.x == 0)
+      for (int w = 1; w < kWarps; ++w) st = join_stats(st, sh[w]);
+  }
+  if (threadIdx.x % (32 * kWarps) != 0) return;
   const float lse = (fabsf(st.x) == INFINITY ? 0.f : st.x) + logf(st.y);
   const int64_t y = a.targets[row];
   const bool inside = y >= 0 && y < a.v, counted = inside && y != a.ignore;
@@ -859,19 +893,21 @@ __global__ void __launch_bounds__(256) vocab_rows_kernel(const VocabRowArgs a) {
   }
 }
 
-// The counted rows' target logits, a warp per row, and the redo flag's clearing.
+// The counted rows' target logits, and the redo flag's clearing. kWarps: as above.
+template <int kWarps>
 __global__ void __launch_bounds__(256)
     vocab_target_kernel(const uint16_t* X, const uint16_t* W, const int64_t* targets, int64_t ignore, int t, int h,
                         int v, float* target_logit, unsigned* redo) {
-  const int row = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  __shared__ float sh[8];
+  const int row = blockIdx.x * (8 / kWarps) + (threadIdx.x >> 5) / kWarps, lane = threadIdx.x & 31;
   if (blockIdx.x == 0 && threadIdx.x == 0) *redo = 0u;
   if (row >= t) return;
   const int64_t y = targets[row];
-  if (y < 0 || y >= v || y == ignore) return;
+  if (y < 0 || y >= v || y == ignore) return;   // (the row's threads alike)
   const uint16_t *x = X + static_cast<int64_t>(row) * h, *w = W + y * h;
   float s = 0.f;
 #pragma unroll 4
-  for (int i = lane; i < (h >> 3); i += 32) {
+  for (int i = threadIdx.x % (32 * kWarps); i < (h >> 3); i += 32 * kWarps) {
     float a[8], b[8];
     unpack8(ldg_vec(x, i), a);
     unpack8(ldg_vec(w, i), b);
@@ -880,7 +916,13 @@ __global__ void __launch_bounds__(256)
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-  if (lane == 0) target_logit[row] = s;
+  if (kWarps > 1) {
+    if (lane == 0) sh[threadIdx.x >> 5] = s;
+    __syncthreads();
+    if (threadIdx.x == 0)
+      for (int w = 1; w < kWarps; ++w) s += sh[w];
+  }
+  if (threadIdx.x % (32 * kWarps) == 0) target_logit[row] = s;
 }
 
 // dX tiles whose K was split: the partial tiles are added in order and rounded once.
