@@ -80,6 +80,7 @@ SIGNATURES = {
     "qlora_linear_fwd_epilogue": (ctypes.c_int, [_PTR, _I64, _PTR, _PTR, _PTR, _I64, ctypes.c_float,
                                                  _PTR, ctypes.c_int, _PTR, _PTR, _PTR, _PTR, _PTR,
                                                  ctypes.c_size_t, _PTR]),
+    "qlora_fwd_epilogue_workspace_bytes": (ctypes.c_size_t, [_I64, _I64, _I64, _I64]),
     "qlora_epilogue_bwd": (ctypes.c_int, [_PTR, _PTR, _I64, _I64, ctypes.c_int, _PTR, _PTR, _PTR,
                                           ctypes.c_size_t, _PTR]),
     "qlora_epilogue_bwd_workspace_bytes": (ctypes.c_size_t, [_I64, _I64]),
@@ -505,7 +506,7 @@ def qlora_linear_fwd_epilogue(X: torch.Tensor, p: PackedNF4, L1: torch.Tensor, L
         Y = _out(dev, Y, bf16, (t, o), "Y")
         Z = _out(dev, Z, bf16, (t, o), "Z", want_Z)
         sT = _out(dev, sT, bf16, (t, r), "sT", want_sT)
-        ws = _scratch(dev, ws, fwd_workspace_bytes(t, h, o, r))
+        ws = _scratch(dev, ws, int(lib().qlora_fwd_epilogue_workspace_bytes(t, h, o, r)))
         d = p.desc()
         _check(lib().qlora_linear_fwd_epilogue(
             ins[0], t, ctypes.byref(d), ins[1], ins[2], r, float(s), ins[3], _act_id(act), ins[4],

@@ -5,6 +5,8 @@
 
 namespace {
 
+constexpr int kMaxSms = 160;   // workspace sizes are host functions: sized for any B200
+
 // ------------------------------------------------------------------------------------------
 // the linear's epilogue
 // ------------------------------------------------------------------------------------------
@@ -65,7 +67,6 @@ NormBwdPlan plan_norm_bwd(int64_t t, int64_t h, int sms) {
   return p;
 }
 
-constexpr int kMaxSms = 160;   // workspace sizes are host functions: sized for any B200
 
 // ------------------------------------------------------------------------------------------
 // vocabulary loss
@@ -376,7 +377,7 @@ int qlora_linear_fwd_epilogue(const uint16_t* X, int64_t t, const nf4_weight* W,
   if (!valid_act(act)) return QLORA_ERR_INVALID_ARG;
   if ((bias && !aligned16(bias)) || (residual && !aligned16(residual)) || (Z_out && !aligned16(Z_out)))
     return QLORA_ERR_MISALIGNED;
-  if (!workspace || ws_bytes < qlora_fwd_workspace_bytes(t, W->in_features, W->out_features, r))
+  if (!workspace || ws_bytes < qlora_fwd_epilogue_workspace_bytes(t, W->in_features, W->out_features, r))
     return QLORA_ERR_WORKSPACE;
   EpilogueArgs e{};
   e.bias = bias;
@@ -384,6 +385,15 @@ int qlora_linear_fwd_epilogue(const uint16_t* X, int64_t t, const nf4_weight* W,
   e.z_out = Z_out;
   e.act = act;
   return fwd_core(X, X, t, W, L1, L2, r, s, Y, sT_out, workspace, reinterpret_cast<cudaStream_t>(stream), &e);
+}
+
+size_t qlora_fwd_epilogue_workspace_bytes(int64_t t, int64_t h, int64_t o, int64_t r) {
+  const size_t base = qlora_fwd_workspace_bytes(t, h, o, r);
+  if (!base || t <= kGemvMaxTokens) return base;
+  // (the shares of a call depend on the card's size: the most any B200 takes)
+  int most = 1;
+  for (int sms = 100; sms <= kMaxSms; ++sms) most = std::max(most, epilogue_shares(t, h, o, sms));
+  return base + (most > 1 ? static_cast<size_t>(most) * t * o * 4 : 0);
 }
 
 size_t qlora_epilogue_bwd_workspace_bytes(int64_t t, int64_t o) {

@@ -76,7 +76,15 @@ struct Nf4GemmArgs {
   Nf4Table tab;
   const uint16_t* addend;  // NULL, or M x N bf16 added to the accumulator before the rounding;
                            // written by the previous kernel on the stream (waited for first)
-  EpilogueArgs epi;        // kEpi only
+  EpilogueArgs epi;        // kEpiFused only
+  int kb_per_split;        // kEpiPartial: weight K-steps of each of gridDim.z shares of K
+};
+
+// What the epilogue does with the accumulator.
+enum GemmEpi : int {
+  kEpiNone = 0,     // bf16 (plus the addend)
+  kEpiFused = 1,    // Z = accumulator + bias, Y = act(Z) + residual; Z stored through tmZ where it is kept
+  kEpiPartial = 2,  // fp32 share of a split K (grid z), through tmZ: M x N x shares
 };
 
 // Wait for an mbarrier phase ignoring the abort flag (used only to drain in-flight copies
@@ -91,9 +99,7 @@ __device__ __forceinline__ void mbar_drain(uint64_t* bar, uint32_t parity) {
   }
 }
 
-// kEpi: Z = accumulator + bias, Y = act(Z) + residual instead of the plain rounding; Z is stored
-// through tmZ where the caller keeps it.
-template <bool kBwd, bool kEpi = false>
+template <bool kBwd, int kEpi = kEpiNone>
 __global__ void __launch_bounds__(tc::kThreads, 1)
     nf4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmP,
                     const __grid_constant__ CUtensorMap tmA2,
@@ -124,7 +130,13 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
   const int n0 = (blockIdx.x >> 1) * BN;                 // the pair's 256 output columns
   const int nh0 = n0 + static_cast<int>(rank) * BNH;    // this CTA's 128 of them
   const int mrow = blockIdx.y * PAIR_M + static_cast<int>(rank) * 128;  // + a * 256
-  const int total = args.num_kb + args.num_lkb;   // weight K-steps, then the LoRA K-steps
+  // weight K-steps (those of this share of K), then the LoRA K-steps (with the last share)
+  const int kb0 = kEpi == kEpiPartial ? static_cast<int>(blockIdx.z) * args.kb_per_split : 0;
+  const int nk = kEpi == kEpiPartial ? min(args.num_kb - kb0, args.kb_per_split) : args.num_kb;
+  const int total = nk + (kEpi != kEpiPartial || blockIdx.z + 1 == gridDim.z ? args.num_lkb : 0);
+  // 256 rows or fewer fill one of the two accumulators
+  const int nacc = args.M - static_cast<int>(blockIdx.y) * PAIR_M > 256 ? 2 : 1;
+  const uint32_t a_bytes = static_cast<uint32_t>(nacc) * A_HALF;
   pdl_launch_dependents();
 
   if (threadIdx.x == 0) {
@@ -169,31 +181,31 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
         if (!mbar_wait(&empty_p[slot], ((kb / P_STAGES) & 1) ^ 1u, abort_flag)) return false;
         mbar_arrive_expect_tx(&full_p[slot], P_BYTES);
         if (!kBwd) {
-          tma_load_2d(sP + slot * P_BYTES, &tmP, &full_p[slot], kb * (BK / 2), nh0);
+          tma_load_2d(sP + slot * P_BYTES, &tmP, &full_p[slot], (kb0 + kb) * (BK / 2), nh0);
         } else {
-          tma_load_2d(sP + slot * P_BYTES, &tmP, &full_p[slot], nh0 / 2, kb * BK);
-          tma_load_2d(sP + slot * P_BYTES + 2048, &tmP, &full_p[slot], nh0 / 2 + 32, kb * BK);
+          tma_load_2d(sP + slot * P_BYTES, &tmP, &full_p[slot], nh0 / 2, (kb0 + kb) * BK);
+          tma_load_2d(sP + slot * P_BYTES + 2048, &tmP, &full_p[slot], nh0 / 2 + 32, (kb0 + kb) * BK);
         }
         codes = kb + 1;
         return true;
       };
-      for (int kb = 0; kb < P_AHEAD && kb < args.num_kb; ++kb) load_codes(kb);   // (free slots: no wait)
+      for (int kb = 0; kb < P_AHEAD && kb < nk; ++kb) load_codes(kb);   // (free slots: no wait)
       for (int i = 0; i < total; ++i) {
         const int slot = i % STAGES;
         const uint32_t ph = (i / STAGES) & 1;
-        if (i + P_AHEAD < args.num_kb && !load_codes(i + P_AHEAD)) break;
+        if (i + P_AHEAD < nk && !load_codes(i + P_AHEAD)) break;
         if (!mbar_wait(&empty[slot], ph ^ 1u, abort_flag)) break;
         uint8_t* a_dst = sA + slot * A_BYTES;
         uint8_t* b_dst = sB + slot * B_BYTES;
         const uint32_t bar = full_a0 + static_cast<uint32_t>(slot * sizeof(uint64_t));
-        if (i >= args.num_kb) {
+        if (i >= nk) {
           // sT / sU come from the kernel launched just before this one, which may still be
           // running (programmatic dependent launch): wait for it before the first LoRA load
-          if (i == args.num_kb) pdl_wait();
-          const int li = i - args.num_kb;
-          if (rank == 0) mbar_arrive_expect_tx(&full_a[slot], 2 * (A_BYTES + B_BYTES));
+          if (i == nk) pdl_wait();
+          const int li = i - nk;
+          if (rank == 0) mbar_arrive_expect_tx(&full_a[slot], 2 * (a_bytes + B_BYTES));
           tma_load_2d_pair(a_dst, &tmA2, bar, li * BK, mrow);
-          tma_load_2d_pair(a_dst + A_HALF, &tmA2, bar, li * BK, mrow + 256);
+          if (nacc == 2) tma_load_2d_pair(a_dst + A_HALF, &tmA2, bar, li * BK, mrow + 256);
           if (!kBwd) {
             // L2 (r x o), MN-major B: this CTA's two 64-column atoms, 8 KB apart
             tma_load_2d_pair(b_dst, &tmB2, bar, nh0, li * BK);
@@ -203,10 +215,9 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
             tma_load_2d_pair(b_dst, &tmB2, bar, li * BK, nh0);
           }
         } else {
-          const int kb = i;
-          if (rank == 0) mbar_arrive_expect_tx(&full_a[slot], 2 * A_BYTES);
-          tma_load_2d_pair(a_dst, &tmA, bar, kb * BK, mrow);
-          tma_load_2d_pair(a_dst + A_HALF, &tmA, bar, kb * BK, mrow + 256);
+          if (rank == 0) mbar_arrive_expect_tx(&full_a[slot], 2 * a_bytes);
+          tma_load_2d_pair(a_dst, &tmA, bar, (kb0 + i) * BK, mrow);
+          if (nacc == 2) tma_load_2d_pair(a_dst + A_HALF, &tmA, bar, (kb0 + i) * BK, mrow + 256);
         }
         issued = i + 1;
       }
@@ -235,7 +246,7 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
         if (!mbar_wait(&full_a[slot], ph, abort_flag)) break;
         if (!mbar_wait(&full_b[slot], ph, abort_flag)) break;
         tc_fence_after();
-        const bool lora = i >= args.num_kb;
+        const bool lora = i >= nk;
         const bool b_mn = lora ? !kBwd : kBwd;
         const uint32_t idesc = lora ? kIdescLora : kIdescMain;
         const uint32_t a_addr = smem_addr(sA + slot * A_BYTES);
@@ -246,6 +257,7 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
                                    : sw128_desc(b_addr + kk * 32, 16, 1024);
 #pragma unroll
           for (int a = 0; a < 2; ++a) {
+            if (a >= nacc) break;
             const uint64_t ad = sw128_desc(a_addr + a * A_HALF + kk * 32, 16, 1024);
             umma2_bf16(tmem_base + a * BN, ad, bd, idesc, (i > 0 || kk > 0) ? 1u : 0u);
           }
@@ -296,7 +308,6 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
     // a ring of registers; the loop below is unrolled by kPf so that every ring index is a
     // compile-time constant and a load is waited for only when its step comes up
     constexpr int kPf = 4;
-    const int nk = args.num_kb;
     uint32_t qr[kPf];
     float sr[kPf];
 #pragma unroll
@@ -305,7 +316,7 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
       qr[j] = 0u;
       sr[j] = 0.f;
       if (valid && i < nk) {
-        const int64_t qi = qbase + static_cast<int64_t>(i) * qstep;
+        const int64_t qi = qbase + static_cast<int64_t>(kb0 + i) * qstep;
         qr[j] = __ldg(args.q8 + qi);
         sr[j] = __ldg(args.s2 + (qi >> 8));
       }
@@ -322,7 +333,7 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
           // codes and table first: they do not depend on the operand slot's MMAs
           const float k = __fmul_rn(static_cast<float>(qr[j]), sr[j]);
           if (valid && i + 2 * kPf < nk) {
-            const int64_t qi = qbase + static_cast<int64_t>(i + 2 * kPf) * qstep;
+            const int64_t qi = qbase + static_cast<int64_t>(kb0 + i + 2 * kPf) * qstep;
             qr[j] = __ldg(args.q8 + qi);
             sr[j] = __ldg(args.s2 + (qi >> 8));
           }
@@ -369,10 +380,38 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
       const uint32_t lane_addr =
           tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(acc * BN);
       uint8_t* stage_tile = smem + warp * 8192;
-      const bool any_row = row0 < args.M;   // warp-uniform: rows past M are not stored
+      const bool any_row = row0 < args.M && acc < nacc;   // warp-uniform: rows past M are not stored
       // N is a multiple of 64, so a round is either wholly inside the output or wholly past it
-      for (int c0 = 0; c0 < BN / 16; c0 += 4) {
-        if (n0 + c0 * 16 >= args.N) break;
+      if (kEpi == kEpiPartial) {
+        // fp32 tiles of 32 x 32 (128-byte rows, swizzled alike), alternating the two staging tiles
+        for (int c0 = 0; c0 < BN && any_row && n0 + c0 < args.N; c0 += 32) {
+          uint8_t* buf = stage_tile + ((c0 >> 5) & 1) * 4096;
+          if (c0 >= 64) {
+            if (lane == 0) bulk_wait_group_read<1>();
+            __syncwarp();
+          }
+          uint32_t v0[16], v1[16];
+          tmem_ld_16(lane_addr + c0, v0);
+          tmem_ld_16(lane_addr + c0 + 16, v1);
+          tmem_ld_wait();
+          uint8_t* rowp = buf + lane * 128;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            *reinterpret_cast<uint4*>(rowp + ((k ^ (lane & 7)) << 4)) =
+                make_uint4(v0[4 * k], v0[4 * k + 1], v0[4 * k + 2], v0[4 * k + 3]);
+            *reinterpret_cast<uint4*>(rowp + (((k + 4) ^ (lane & 7)) << 4)) =
+                make_uint4(v1[4 * k], v1[4 * k + 1], v1[4 * k + 2], v1[4 * k + 3]);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_3d(&tmZ, buf, n0 + c0, row0, static_cast<int>(blockIdx.z));
+            bulk_commit_group();
+          }
+        }
+      }
+      for (int c0 = 0; kEpi != kEpiPartial && c0 < BN / 16; c0 += 4) {
+        if (n0 + c0 * 16 >= args.N || !any_row) break;
         uint8_t* buf = stage_tile + ((c0 >> 2) & 1) * 4096;
         if (c0 >= 8) {   // the store issued from this tile two rounds ago has read it
           if (lane == 0) bulk_wait_group_read<1>();
@@ -398,7 +437,7 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
             }
           }
           uint8_t* rowp = buf + lane * 128;
-          if (kEpi) {
+          if (kEpi == kEpiFused) {
             const int col = n0 + (c0 + q) * 16;
             float z[16];
 #pragma unroll
@@ -446,9 +485,9 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0 && any_row) {
+        if (lane == 0) {
           tma_store_2d(&tmOut, buf, n0 + c0 * 16, row0);
-          if (kEpi && args.epi.z_out) tma_store_2d(&tmZ, buf + kEpiZTile, n0 + c0 * 16, row0);
+          if (kEpi == kEpiFused && args.epi.z_out) tma_store_2d(&tmZ, buf + kEpiZTile, n0 + c0 * 16, row0);
           bulk_commit_group();
         }
       }
@@ -465,6 +504,36 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
   }
   // completion stays in stream order even when an abort skipped the wait before the LoRA steps
   if (threadIdx.x == 0) pdl_wait();
+}
+
+// The fused epilogue over a split K's shares (shares x M x N fp32, added in order): eight columns of a
+// row per thread.
+__global__ void __launch_bounds__(256)
+    nf4_gemm_join_kernel(const float* part, int shares, uint16_t* Y, int64_t rows, int N, const EpilogueArgs epi) {
+  const int64_t vec = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x, nvec = N >> 3;
+  if (vec >= rows * nvec) return;
+  float z[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int p = 0; p < shares; ++p) {
+    const float4* q = reinterpret_cast<const float4*>(part + p * rows * N) + 2 * vec;
+    const float4 u = __ldcg(q), w = __ldcg(q + 1);
+    z[0] += u.x; z[1] += u.y; z[2] += u.z; z[3] += u.w;
+    z[4] += w.x; z[5] += w.y; z[6] += w.z; z[7] += w.w;
+  }
+  float b[8];
+  if (epi.bias) {
+    unpack8(ldg_vec(epi.bias, vec % nvec), b);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) z[k] += b[k];
+  }
+  if (epi.z_out) reinterpret_cast<uint4*>(epi.z_out)[vec] = pack8(z);
+  act_apply(z, epi.act);
+  if (epi.residual) {
+    unpack8(ldg_vec(epi.residual, vec), b);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) z[k] += b[k];
+  }
+  reinterpret_cast<uint4*>(Y)[vec] = pack8(z);
 }
 
 }  // namespace qlora

@@ -249,6 +249,13 @@ __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void*
       ::"l"(reinterpret_cast<uint64_t>(map)), "r"(smem_addr(smem_src)), "r"(x), "r"(y)
       : "memory");
 }
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* smem_src, int32_t x, int32_t y,
+                                             int32_t z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];"
+      ::"l"(reinterpret_cast<uint64_t>(map)), "r"(smem_addr(smem_src)), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
 // Copy `bytes` (a multiple of 16, both addresses 16-byte aligned) from shared to global memory
 // (written by generic stores and made visible with fence_proxy_async_smem first). Tracked by
 // bulk groups like the tensor stores.

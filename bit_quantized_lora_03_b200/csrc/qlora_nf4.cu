@@ -213,7 +213,9 @@ int current_device(int* dev_out) {
                                  static_cast<int>(tc::nf4_gemm_smem_bytes())) == cudaSuccess;
     fine &= cudaFuncSetAttribute(nf4_gemm_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  static_cast<int>(tc::nf4_gemm_smem_bytes())) == cudaSuccess;
-    fine &= cudaFuncSetAttribute(nf4_gemm_kernel<false, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    fine &= cudaFuncSetAttribute(nf4_gemm_kernel<false, kEpiFused>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 static_cast<int>(tc::nf4_gemm_smem_bytes())) == cudaSuccess;
+    fine &= cudaFuncSetAttribute(nf4_gemm_kernel<false, kEpiPartial>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  static_cast<int>(tc::nf4_gemm_smem_bytes())) == cudaSuccess;
     fine &= cudaFuncSetAttribute(nf4_gemv_kernel<1, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  static_cast<int>(gv::smem_bytes())) == cudaSuccess;
@@ -361,6 +363,19 @@ bool make_map_2d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base, 
   return r == CUDA_SUCCESS;
 }
 
+// fp32 planes (z) of row-major matrices, 32 x 32 boxes, for stores that are cut off at each plane's edge.
+bool map_f32_planes(CUtensorMap* map, const float* base, uint64_t cols, uint64_t rows, uint64_t planes) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {cols, rows, planes};
+  const cuuint64_t strides[2] = {cols * 4, cols * 4 * rows};
+  const cuuint32_t box[3] = {32, 32, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<float*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool map_bf16(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint32_t box_cols,
               uint32_t box_rows) {
   return make_map_2d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, cols, rows, cols * 2, box_cols,
@@ -421,6 +436,29 @@ GemvWs carve_gemv(void* base, int64_t t, int64_t o, int64_t r) {
 }
 
 constexpr int64_t kGemvMaxTokens = 16;
+
+// Shares of K of the linear with the fused epilogue (t > kGemvMaxTokens): its tiles of 512 tokens x 256
+// outputs leave most of the card idle for a few hundred tokens. A K-step takes about 0.75 us (0.45 with
+// one accumulator), a round of pairs as long as a tile's share; the shares cost their fp32 traffic at some
+// 5 TB/s and another launch. 4096 -> 4096: 17 tokens 64 -> 22 us;
+// 11008 -> 4096: 777 tokens 150 -> 93 us.
+int epilogue_shares(int64_t t, int64_t h, int64_t o, int sms) {
+  const int64_t tiles = (t + 511) / 512 * ((o + 255) / 256), kb = h / 64, pairs = sms / 2;
+  const double step = t > 256 ? 0.75 : 0.45;
+  int best = 1;
+  double cost = 0.0;
+  for (int s = 1; s <= 16 && kb / s >= 4; ++s) {
+    const int64_t per = (kb + s - 1) / s;
+    if (s > 1 && per * (s - 1) >= kb) continue;   // a share would be empty
+    const double c = static_cast<double>((tiles * s + pairs - 1) / pairs) * (per * step + 5.0) +
+                     (s > 1 ? 8.0 * s * t * o / 5e6 + 4.0 : 0.0);
+    if (s == 1 || c < cost) {
+      cost = c;
+      best = s;
+    }
+  }
+  return best;
+}
 
 // ------------------------------------------------------------------------------------------
 // launch helpers
@@ -550,22 +588,25 @@ LoraWs carve_lora(void* base, int64_t, int64_t) {
 
 // The fused NF4 GEMM runs as clusters of 2 CTAs (cta_group::2): grid x = 2 CTAs per 256-column
 // tile, grid y = 512-token row blocks.
-template <bool kBwd, bool kEpi = false>
+template <bool kBwd, int kEpi = kEpiNone>
 int launch_nf4_gemm(const CUtensorMap& mA, const CUtensorMap& mP, const CUtensorMap& mA2,
                     const CUtensorMap& mB2, const Nf4GemmArgs& ga, int64_t t, int64_t ncols,
-                    cudaStream_t st, int prof_kind) {
+                    cudaStream_t st, int prof_kind, int shares = 1, const float* part = nullptr) {
   // the output (t x ncols bf16) as 32-row x 64-column boxes for the epilogue's TMA stores
   CUtensorMap mOut;
   if (!map_bf16(&mOut, ga.out, static_cast<uint64_t>(ncols), static_cast<uint64_t>(t), 64, 32))
     return QLORA_ERR_CUDA;
-  CUtensorMap mZ = mOut;   // a filler unless Z is kept
-  if (kEpi && ga.epi.z_out &&
+  CUtensorMap mZ = mOut;   // a filler unless Z or shares are stored
+  if (kEpi == kEpiFused && ga.epi.z_out &&
       !map_bf16(&mZ, ga.epi.z_out, static_cast<uint64_t>(ncols), static_cast<uint64_t>(t), 64, 32))
+    return QLORA_ERR_CUDA;
+  if (kEpi == kEpiPartial && !map_f32_planes(&mZ, part, static_cast<uint64_t>(ncols), static_cast<uint64_t>(t),
+                                             static_cast<uint64_t>(shares)))
     return QLORA_ERR_CUDA;
   if ((t + tc::PAIR_M - 1) / tc::PAIR_M > 65535) return QLORA_ERR_BAD_SHAPE;  // grid y limit
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(2 * ((ncols + tc::BN - 1) / tc::BN)),
-                     static_cast<unsigned>((t + tc::PAIR_M - 1) / tc::PAIR_M), 1);
+                     static_cast<unsigned>((t + tc::PAIR_M - 1) / tc::PAIR_M), static_cast<unsigned>(shares));
   cfg.blockDim = dim3(tc::kThreads, 1, 1);
   cfg.dynamicSmemBytes = tc::nf4_gemm_smem_bytes();
   cfg.stream = st;
@@ -774,7 +815,15 @@ int fwd_core(const uint16_t* X, const uint16_t* Xl, int64_t t, const nf4_weight*
   ga.tab = device_table();
   if (epi) {
     ga.epi = *epi;
-    return launch_nf4_gemm<false, true>(mA, mP, mA2, mB2, ga, t, o, st, prof::kGemmFwd);
+    const int shares = epilogue_shares(t, h, o, sms);
+    if (shares == 1) return launch_nf4_gemm<false, kEpiFused>(mA, mP, mA2, mB2, ga, t, o, st, prof::kGemmFwd);
+    float* part = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(workspace) + lora_region_bytes(t, r));
+    ga.kb_per_split = (ga.num_kb + shares - 1) / shares;
+    if ((rc = launch_nf4_gemm<false, kEpiPartial>(mA, mP, mA2, mB2, ga, t, o, st, prof::kGemmFwd, shares, part)))
+      return rc;
+    nf4_gemm_join_kernel<<<static_cast<unsigned>((t * (o / 8) + 255) / 256), 256, 0, st>>>(part, shares, Y, t,
+                                                                                         ga.N, ga.epi);
+    return launch_status();
   }
   return launch_nf4_gemm<false>(mA, mP, mA2, mB2, ga, t, o, st, prof::kGemmFwd);
 }

@@ -354,8 +354,9 @@ QLORA_API int qlora_adamw_step_multi(int ntensors, float *const *params, uint16_
  *   residual  device bf16, t x o row-major, or NULL. It may be Y itself (updated in place); any
  *             other overlap of an output with an input is not allowed.
  *   Z_out     device bf16, t x o (output, bf16(Z), kept for qlora_epilogue_bwd) or NULL.
- * Every other argument, the workspace (qlora_fwd_workspace_bytes) and the errors are those of
- * qlora_linear_fwd; an unknown act gives INVALID_ARG. */
+ *   workspace, ws_bytes: at least qlora_fwd_epilogue_workspace_bytes(t, h, o, r) bytes.
+ * Every other argument and the errors are those of qlora_linear_fwd; an unknown act gives
+ * INVALID_ARG. */
 #define QLORA_ACT_NONE 0
 #define QLORA_ACT_RELU 1
 #define QLORA_ACT_GELU 2
@@ -366,6 +367,7 @@ QLORA_API int qlora_linear_fwd_epilogue(const uint16_t *X, int64_t t, const nf4_
                                         const uint16_t *bias, int act, const uint16_t *residual,
                                         uint16_t *Y, uint16_t *Z_out, uint16_t *sT_out,
                                         void *workspace, size_t ws_bytes, qlora_stream_t stream);
+QLORA_API size_t qlora_fwd_epilogue_workspace_bytes(int64_t t, int64_t h, int64_t o, int64_t r);
 
 /* qlora_epilogue_bwd -- the backward of that epilogue: dZ = dY . act'(Z) (elementwise) and
  * db = sum over tokens of dZ. dZ then takes dY's place in qlora_linear_bwd; the residual's

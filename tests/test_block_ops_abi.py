@@ -29,6 +29,10 @@ def test_linear_epilogue(lib):
     assert f(w=B.NF4WeightDesc(P, P, P, 100, 128)) == SHAPE
     assert f(bias=P + 2) == f(R=P + 8) == f(Z=P + 4) == f(X=P + 2) == ALIGN
     assert f(ws=None) == f(n=64) == WS
+    # a few hundred tokens split K: their fp32 shares lie behind the plain forward's workspace
+    assert lib.qlora_fwd_epilogue_workspace_bytes(4, 128, 128, 16) == lib.qlora_fwd_workspace_bytes(4, 128, 128, 16)
+    assert lib.qlora_fwd_epilogue_workspace_bytes(64, 4096, 4096, 64) >= 2 * 64 * 4096 * 4
+    assert lib.qlora_fwd_epilogue_workspace_bytes(64, 100, 128, 16) == 0
 
 
 def test_epilogue_backward(lib):

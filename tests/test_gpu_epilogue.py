@@ -41,6 +41,9 @@ CASES = [  # t, h, o, r, act, bias, residual, Z kept
     (17, 320, 576, 48, "relu", True, True, True), (300, 320, 576, 48, "silu", True, False, True),
     (513, 640, 320, 80, "none", False, True, False), (257, 64, 64, 16, "gelu", True, True, False),
     (1030, 192, 832, 64, "gelu_tanh", False, False, True), (40, 128, 256, 16, "none", True, False, True),
+    # K split over the card: one and two accumulators, shares of unequal length, two row tiles
+    (23, 4096, 512, 64, "silu", True, True, True), (300, 2112, 320, 16, "gelu", True, True, False),
+    (700, 1984, 192, 48, "none", False, True, True), (129, 11008, 256, 80, "relu", True, False, False),
 ]
 
 
