@@ -390,19 +390,33 @@ __global__ void __launch_bounds__(gv::kThreads, 1)
     const int e = i >> 5;
     table[i] = make_float2(args.tab.level[e >> 4], args.tab.level[e & 15]);
   }
-  // sT = bf16(s . X.L1) from the LoRA-down kernel's partial sums (launched just before this
-  // kernel, which may start early: wait for its completion and memory first)
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  for (int i = threadIdx.x; i < args.t * args.r; i += kThreads) {
-    float v = 0.f;
+  // sT = bf16(s . X.L1) from the LoRA-down kernel's partial sums, once per CTA, by all its warps.
+  // That kernel is launched just before this one, which may start early: wait for its completion
+  // and memory first. Nothing needs either before a warp's first sums are added (to a buffer that
+  // kernel zeroes). For 9 to 16 tokens, where it takes 12 us (8192 inputs, rank 64), every warp comes
+  // here only then, most of its work behind it; for up to 8 it is done by the time the table is, and
+  // joining later would only lengthen the end (24.7 against 26.7 us for one token, 4096 x 11008).
+  auto join_lora = [&]() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    for (int i = threadIdx.x; i < args.t * args.r; i += kThreads) {
+      float v = 0.f;
 #pragma unroll
-    for (int p = 0; p < kDownParts; ++p) v += __ldcg(args.Tpart + p * args.t * args.r + i);
-    const uint16_t b = __bfloat16_as_ushort(__float2bfloat16_rn(args.s * v));
-    sts[(i / args.r) * kMaxRank + i % args.r] = b;
-    if (blockIdx.x == 0 && args.sT_out) args.sT_out[i] = b;
+      for (int p = 0; p < kDownParts; ++p) v += __ldcg(args.Tpart + p * args.t * args.r + i);
+      const uint16_t b = __bfloat16_as_ushort(__float2bfloat16_rn(args.s * v));
+      sts[(i / args.r) * kMaxRank + i % args.r] = b;
+      if (blockIdx.x == 0 && args.sT_out) args.sT_out[i] = b;
+    }
+    __syncthreads();
+  };
+  bool joined = NT == 1;
+  if (joined)
+    join_lora();
+  else
+    __syncthreads();
+  if (nrun <= 0) {
+    if (!joined) join_lora();
+    return;
   }
-  __syncthreads();
-  if (nrun <= 0) return;
 
   const uint32_t lane_slot = tab + static_cast<uint32_t>(lane) * 8u;
   float acc[2][NT][4];
@@ -434,7 +448,10 @@ __global__ void __launch_bounds__(gv::kThreads, 1)
       }
     const int64_t row0 = cur.tile * kTileRows;
     for (int u = cur.u0; u < cur.u1; ++u) {
-      if (!mbar_wait(&bars[e], ph, &abort_flag)) return;
+      if (!mbar_wait_warp(&bars[e], ph, &abort_flag)) {
+        if (!joined) join_lora();
+        return;
+      }
       GemvCodes cc;
       gemv_read_codes(cc, slot + kSlotCodes + e * kUnitBytes, g, q);
       __syncwarp();  // every lane has read the entry before it is refilled
@@ -483,6 +500,8 @@ __global__ void __launch_bounds__(gv::kThreads, 1)
     }
     tile_units += cur.u1 - cur.u0;
     if (nxt.u0 == nxt.u1 || nxt.tile != cur.tile) {
+      if (!joined) join_lora();
+      joined = true;
       // add the tile's sums, then count its units; the warp that completes the tile
       // finishes it (the fence makes this warp's sums visible before its count)
       gemv_flush<NT>(acc, args, cur.tile, g, q);
@@ -521,8 +540,9 @@ constexpr int kClusterCtas = 8;
 constexpr int kClusters = gv::kDownParts;
 constexpr int kCtas = kClusterCtas * kClusters;
 constexpr int kThreads = 256;
+constexpr int kPiecePairs = 256;   // input pairs staged at a time
 constexpr size_t smem_bytes(int t, int r) {
-  return (static_cast<size_t>(2 * kThreads) * t + static_cast<size_t>(t) * r) * 4;
+  return (static_cast<size_t>(2 * kThreads) * t + static_cast<size_t>(t) * r + static_cast<size_t>(kPiecePairs) * t) * 4;
 }
 }  // namespace gd
 
@@ -548,37 +568,51 @@ __global__ void __cluster_dims__(gd::kClusterCtas, 1, 1) __launch_bounds__(gd::k
   }
 
   const int ncp = r / 2;                // column pairs
-  const int nkg = gd::kThreads / ncp;   // k strides (r <= 256, r % 16 == 0: exact)
+  const int nkg = gd::kThreads / ncp;   // k strides
   const int cp = tid % ncp, kg = tid / ncp;
-  // this CTA's inputs: an even share of the 2-row pairs
+  // this CTA's inputs: an even share of the 2-row pairs, walked in pieces whose activations (t x
+  // piece) are staged in shared memory by coalesced loads: read one by one where they are used,
+  // they cost a dependent load of 4 bytes for every token and pair
   const int64_t pairs = h / 2;
   const int64_t p0 = pairs * blockIdx.x / gd::kCtas, p1 = pairs * (blockIdx.x + 1) / gd::kCtas;
+  uint32_t* xs = reinterpret_cast<uint32_t*>(dsm) + static_cast<size_t>(2 * gd::kThreads) * t + static_cast<size_t>(t) * r;
+  const int piece = gd::kPiecePairs / (4 * nkg) * (4 * nkg);   // whole rounds of the loop below
   float acc[16][2];
 #pragma unroll
   for (int n = 0; n < 16; ++n) acc[n][0] = acc[n][1] = 0.f;
-  for (int64_t pb = p0 + kg; pb < p1; pb += 4 * nkg) {
-    uint32_t la[4], lb[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int64_t pr = pb + u * nkg;
-      const int64_t k = 2 * (pr < p1 ? pr : p0);
-      la[u] = __ldg(reinterpret_cast<const uint32_t*>(L1 + k * r) + cp);
-      lb[u] = __ldg(reinterpret_cast<const uint32_t*>(L1 + (k + 1) * r) + cp);
+  for (int64_t pp = p0; pp < p1; pp += piece) {
+    const int64_t pe = pp + piece < p1 ? pp + piece : p1;
+    const int np = static_cast<int>(pe - pp);
+    if (pp > p0) __syncthreads();   // the piece before has been read
+    for (int n = tid >> 5; n < t; n += gd::kThreads / 32) {
+      const uint32_t* xr = reinterpret_cast<const uint32_t*>(X + static_cast<int64_t>(n) * h) + pp;
+      for (int i = tid & 31; i < np; i += 32) xs[n * gd::kPiecePairs + i] = __ldg(xr + i);
     }
+    __syncthreads();
+    for (int64_t pb = pp + kg; pb < pe; pb += 4 * nkg) {
+      uint32_t la[4], lb[4];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int64_t pr = pb + u * nkg;
-      if (pr >= p1) break;
-      const int64_t k = 2 * pr;
-      const float a0 = bf16_bits_to_float(la[u] & 0xffffu), a1 = bf16_bits_to_float(la[u] >> 16);
-      const float b0 = bf16_bits_to_float(lb[u] & 0xffffu), b1 = bf16_bits_to_float(lb[u] >> 16);
+      for (int u = 0; u < 4; ++u) {
+        const int64_t pr = pb + u * nkg;
+        const int64_t k = 2 * (pr < p1 ? pr : p0);
+        la[u] = __ldg(reinterpret_cast<const uint32_t*>(L1 + k * r) + cp);
+        lb[u] = __ldg(reinterpret_cast<const uint32_t*>(L1 + (k + 1) * r) + cp);
+      }
 #pragma unroll
-      for (int n = 0; n < 16; ++n) {
-        if (n < t) {
-          const uint32_t xv = __ldg(reinterpret_cast<const uint32_t*>(X + static_cast<int64_t>(n) * h + k));
-          const float x0 = bf16_bits_to_float(xv & 0xffffu), x1 = bf16_bits_to_float(xv >> 16);
-          acc[n][0] = fmaf(x1, b0, fmaf(x0, a0, acc[n][0]));
-          acc[n][1] = fmaf(x1, b1, fmaf(x0, a1, acc[n][1]));
+      for (int u = 0; u < 4; ++u) {
+        const int64_t pr = pb + u * nkg;
+        if (pr >= p1) break;
+        const float a0 = bf16_bits_to_float(la[u] & 0xffffu), a1 = bf16_bits_to_float(la[u] >> 16);
+        const float b0 = bf16_bits_to_float(lb[u] & 0xffffu), b1 = bf16_bits_to_float(lb[u] >> 16);
+        const uint32_t* xp = xs + static_cast<int>(pr - pp);
+#pragma unroll
+        for (int n = 0; n < 16; ++n) {
+          if (n < t) {
+            const uint32_t xv = xp[n * gd::kPiecePairs];
+            const float x0 = bf16_bits_to_float(xv & 0xffffu), x1 = bf16_bits_to_float(xv >> 16);
+            acc[n][0] = fmaf(x1, b0, fmaf(x0, a0, acc[n][0]));
+            acc[n][1] = fmaf(x1, b1, fmaf(x0, a1, acc[n][1]));
+          }
         }
       }
     }
