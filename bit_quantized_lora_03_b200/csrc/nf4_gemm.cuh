@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
                     const __grid_constant__ CUtensorMap tmA2,
                     const __grid_constant__ CUtensorMap tmB2,
                     const __grid_constant__ CUtensorMap tmOut, const __grid_constant__ CUtensorMap tmZ,
-                    const Nf4GemmArgs args) {
+                    const __grid_constant__ CUtensorMap tmR, const Nf4GemmArgs args) {
   using namespace tc;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -195,6 +195,10 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
         const uint32_t ph = (i / STAGES) & 1;
         if (i + P_AHEAD < nk && !load_codes(i + P_AHEAD)) break;
         if (!mbar_wait(&empty[slot], ph ^ 1u, abort_flag)) break;
+        if (kEpi == kEpiFused && args.epi.residual && i == (total > 16 ? total - 16 : 0)) {
+          for (int a = 0; a < nacc; ++a)       // this CTA's 128 rows of each accumulator, 256 columns
+            for (int c = 0; c < BN && n0 + c < args.N; c += 64) tma_prefetch_2d(&tmR, n0 + c, mrow + a * 256);
+        }
         uint8_t* a_dst = sA + slot * A_BYTES;
         uint8_t* b_dst = sB + slot * B_BYTES;
         const uint32_t bar = full_a0 + static_cast<uint32_t>(slot * sizeof(uint64_t));
@@ -370,6 +374,20 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
     // one TMA store of the tile: whole 128-byte lines instead of 32 scattered row pieces per
     // store instruction. Two staging tiles per warp (8 KB, in the drained stage buffers) let a
     // round's shared-memory writes overlap the previous round's store.
+    // The fused epilogue walks 16 columns at a time in a loop that is not unrolled: its code runs a few
+    // times per CTA, and 64 columns of straight-line code per activation took longer to fetch than to
+    // execute. Bias and residual run one step ahead, the first ones ahead of the last products.
+    const int epi_row0 = mrow + (warp >> 2) * 256 + (warp & 3) * 32, epi_row = epi_row0 + lane;
+    uint4 rq[2], bq[2];
+    auto epi_load = [&](int col) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        if (args.epi.bias) bq[k] = ldg_vec(args.epi.bias, (col >> 3) + k);
+        if (args.epi.residual && epi_row < args.M)
+          rq[k] = ldg_vec(args.epi.residual, ((static_cast<int64_t>(epi_row) * args.N + col) >> 3) + k);
+      }
+    };
+    if (kEpi == kEpiFused && epi_row0 < args.M) epi_load(n0);
     const bool done = mbar_wait_warp(acc_full, 0, abort_flag);
     tc_fence_after();
     if (__shfl_sync(0xFFFFFFFFu, done && !*abort_flag, 0)) {
@@ -410,7 +428,60 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
           }
         }
       }
-      for (int c0 = 0; kEpi != kEpiPartial && c0 < BN / 16; c0 += 4) {
+      if (kEpi == kEpiFused && any_row) {
+        const int cols = min(BN, args.N - n0);   // a multiple of 64
+        uint32_t v[16];
+        tmem_ld_16(lane_addr, v);
+#pragma unroll 1
+        for (int c = 0; c < cols; c += 16) {
+          uint8_t* buf = stage_tile + ((c >> 6) & 1) * 4096;
+          if (c >= 128 && (c & 63) == 0) {   // the stores issued from this tile two rounds ago have read it
+            if (lane == 0) bulk_wait_group_read<1>();
+            __syncwarp();
+          }
+          tmem_ld_wait();
+          float z[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) z[k] = __uint_as_float(v[k]);
+          const uint4 r0 = rq[0], r1 = rq[1], b0 = bq[0], b1 = bq[1];
+          if (c + 16 < cols) {
+            tmem_ld_16(lane_addr + c + 16, v);
+            epi_load(n0 + c + 16);
+          }
+          uint8_t* at0 = buf + lane * 128 + ((((c >> 3) & 7) ^ (lane & 7)) << 4);   // swizzled 16-byte chunks
+          uint8_t* at1 = buf + lane * 128 + (((((c >> 3) & 7) + 1) ^ (lane & 7)) << 4);
+          float f[16];
+          if (args.epi.bias) {
+            unpack8(b0, *reinterpret_cast<float(*)[8]>(&f[0]));
+            unpack8(b1, *reinterpret_cast<float(*)[8]>(&f[8]));
+#pragma unroll
+            for (int k = 0; k < 16; ++k) z[k] += f[k];
+          }
+          if (args.epi.z_out) {
+            *reinterpret_cast<uint4*>(at0 + kEpiZTile) = pack8(*reinterpret_cast<const float(*)[8]>(&z[0]));
+            *reinterpret_cast<uint4*>(at1 + kEpiZTile) = pack8(*reinterpret_cast<const float(*)[8]>(&z[8]));
+          }
+          act_apply(z, args.epi.act);
+          if (args.epi.residual) {   // (rows behind M: not stored)
+            unpack8(r0, *reinterpret_cast<float(*)[8]>(&f[0]));
+            unpack8(r1, *reinterpret_cast<float(*)[8]>(&f[8]));
+#pragma unroll
+            for (int k = 0; k < 16; ++k) z[k] += f[k];
+          }
+          *reinterpret_cast<uint4*>(at0) = pack8(*reinterpret_cast<const float(*)[8]>(&z[0]));
+          *reinterpret_cast<uint4*>(at1) = pack8(*reinterpret_cast<const float(*)[8]>(&z[8]));
+          if ((c & 63) == 48) {   // a 64-column tile is complete
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_2d(&tmOut, buf, n0 + c - 48, row0);
+              if (args.epi.z_out) tma_store_2d(&tmZ, buf + kEpiZTile, n0 + c - 48, row0);
+              bulk_commit_group();
+            }
+          }
+        }
+      }
+      for (int c0 = 0; kEpi == kEpiNone && c0 < BN / 16; c0 += 4) {
         if (n0 + c0 * 16 >= args.N || !any_row) break;
         uint8_t* buf = stage_tile + ((c0 >> 2) & 1) * 4096;
         if (c0 >= 8) {   // the store issued from this tile two rounds ago has read it
@@ -437,40 +508,6 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
             }
           }
           uint8_t* rowp = buf + lane * 128;
-          if (kEpi == kEpiFused) {
-            const int col = n0 + (c0 + q) * 16;
-            float z[16];
-#pragma unroll
-            for (int k = 0; k < 16; ++k) z[k] = __uint_as_float(v[k]);
-            if (args.epi.bias) {
-#pragma unroll
-              for (int g = 0; g < 2; ++g) {
-                float b[8];
-                unpack8(ldg_vec(args.epi.bias, (col >> 3) + g), b);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) z[8 * g + k] += b[k];
-              }
-            }
-            if (args.epi.z_out) {
-#pragma unroll
-              for (int g = 0; g < 2; ++g)
-                *reinterpret_cast<uint4*>(rowp + kEpiZTile + (((2 * q + g) ^ (lane & 7)) << 4)) =
-                    make_uint4(pack_bf16x2(z[8 * g], z[8 * g + 1]), pack_bf16x2(z[8 * g + 2], z[8 * g + 3]),
-                               pack_bf16x2(z[8 * g + 4], z[8 * g + 5]), pack_bf16x2(z[8 * g + 6], z[8 * g + 7]));
-            }
-            act_apply(z, args.epi.act);
-            if (args.epi.residual && row < args.M) {
-#pragma unroll
-              for (int g = 0; g < 2; ++g) {
-                float b[8];
-                unpack8(ldg_vec(args.epi.residual, ((static_cast<int64_t>(row) * args.N + col) >> 3) + g), b);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) z[8 * g + k] += b[k];
-              }
-            }
-#pragma unroll
-            for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(z[k]);
-          }
           uint4 o0, o1;
           o0.x = pack_bf16x2(__uint_as_float(v[0]), __uint_as_float(v[1]));
           o0.y = pack_bf16x2(__uint_as_float(v[2]), __uint_as_float(v[3]));
@@ -487,7 +524,6 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
         __syncwarp();
         if (lane == 0) {
           tma_store_2d(&tmOut, buf, n0 + c0 * 16, row0);
-          if (kEpi == kEpiFused && args.epi.z_out) tma_store_2d(&tmZ, buf + kEpiZTile, n0 + c0 * 16, row0);
           bulk_commit_group();
         }
       }

@@ -221,6 +221,13 @@ __device__ __forceinline__ void tma_load_2d(void* smem_dst, const CUtensorMap* m
       : "memory");
 }
 
+// Brings the box at (x, y) into L2 (no shared memory, nothing to wait for).
+__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap* map, int32_t x, int32_t y) {
+  asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y)
+               : "memory");
+}
+
 // The shared::cluster address of the same shared-memory offset in CTA `rank` of this cluster.
 __device__ __forceinline__ uint32_t cluster_smem_addr(const void* local, uint32_t rank) {
   uint32_t raddr;

@@ -600,6 +600,10 @@ int launch_nf4_gemm(const CUtensorMap& mA, const CUtensorMap& mP, const CUtensor
   if (kEpi == kEpiFused && ga.epi.z_out &&
       !map_bf16(&mZ, ga.epi.z_out, static_cast<uint64_t>(ncols), static_cast<uint64_t>(t), 64, 32))
     return QLORA_ERR_CUDA;
+  CUtensorMap mR = mOut;   // a filler unless there is a residual
+  if (kEpi == kEpiFused && ga.epi.residual &&
+      !map_bf16(&mR, ga.epi.residual, static_cast<uint64_t>(ncols), static_cast<uint64_t>(t), 64, 128))
+    return QLORA_ERR_CUDA;
   if (kEpi == kEpiPartial && !map_f32_planes(&mZ, part, static_cast<uint64_t>(ncols), static_cast<uint64_t>(t),
                                              static_cast<uint64_t>(shares)))
     return QLORA_ERR_CUDA;
@@ -624,7 +628,7 @@ int launch_nf4_gemm(const CUtensorMap& mA, const CUtensorMap& mP, const CUtensor
   cudaError_t e;
   {
     prof::Scope ps(prof_kind, st);
-    e = cudaLaunchKernelEx(&cfg, nf4_gemm_kernel<kBwd, kEpi>, mA, mP, mA2, mB2, mOut, mZ, ga);
+    e = cudaLaunchKernelEx(&cfg, nf4_gemm_kernel<kBwd, kEpi>, mA, mP, mA2, mB2, mOut, mZ, mR, ga);
   }
   if (e != cudaSuccess) {
     cudaGetLastError();
