@@ -244,28 +244,31 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
       constexpr uint32_t kIdescMain = idesc_bf16(256, BN, false, kBwd);
       constexpr uint32_t kIdescLora = idesc_bf16(256, BN, false, !kBwd);
       bool any = false;
+      const uint32_t a_lo0 = sw128_desc_lo(smem_addr(sA), 16);
+      const uint32_t b_lo_k = sw128_desc_lo(smem_addr(sB), 16), b_lo_mn = sw128_desc_lo(smem_addr(sB), 8192);
       for (int i = 0; i < total; ++i) {
         const int slot = i % STAGES;
         const uint32_t ph = (i / STAGES) & 1;
         if (!mbar_wait(&full_a[slot], ph, abort_flag)) break;
         if (!mbar_wait(&full_b[slot], ph, abort_flag)) break;
         tc_fence_after();
-        const bool lora = i >= nk;
-        const bool b_mn = lora ? !kBwd : kBwd;
-        const uint32_t idesc = lora ? kIdescLora : kIdescMain;
-        const uint32_t a_addr = smem_addr(sA + slot * A_BYTES);
-        const uint32_t b_addr = smem_addr(sB + slot * B_BYTES);
+        // A is K-major; B (the weights forward, L1 backward) K-major or (L2 forward, the weights
+        // backward) MN-major
+        const uint32_t a_lo = a_lo0 + slot * (A_BYTES >> 4), b_off = slot * (B_BYTES >> 4);
+        auto issue = [&](uint32_t b_lo, uint32_t b_step, uint32_t idesc) {
 #pragma unroll
-        for (int kk = 0; kk < BK / 16; ++kk) {
-          const uint64_t bd = b_mn ? sw128_desc(b_addr + kk * 2048, 8192, 1024)
-                                   : sw128_desc(b_addr + kk * 32, 16, 1024);
-#pragma unroll
-          for (int a = 0; a < 2; ++a) {
-            if (a >= nacc) break;
-            const uint64_t ad = sw128_desc(a_addr + a * A_HALF + kk * 32, 16, 1024);
-            umma2_bf16(tmem_base + a * BN, ad, bd, idesc, (i > 0 || kk > 0) ? 1u : 0u);
+          for (int kk = 0; kk < BK / 16; ++kk) {
+            const uint64_t bd = sw128_desc_of(b_lo + kk * b_step);
+            umma2_bf16(tmem_base, sw128_desc_of(a_lo + kk * 2), bd, idesc, (i > 0 || kk > 0) ? 1u : 0u);
+            if (nacc == 2)
+              umma2_bf16(tmem_base + BN, sw128_desc_of(a_lo + (A_HALF >> 4) + kk * 2), bd, idesc,
+                         (i > 0 || kk > 0) ? 1u : 0u);
           }
-        }
+        };
+        if ((i >= nk) == kBwd)
+          issue(b_lo_k + b_off, 2, i >= nk ? kIdescLora : kIdescMain);
+        else
+          issue(b_lo_mn + b_off, 128, i >= nk ? kIdescLora : kIdescMain);
         umma2_commit_multicast(&empty[slot], 0x3);   // frees the stage in both CTAs
         any = true;
       }

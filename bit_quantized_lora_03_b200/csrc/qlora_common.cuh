@@ -399,6 +399,20 @@ __device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr, uint32_t lbo, uin
   return d;
 }
 
+// The same descriptor in two halves, for loops over a ring of stages: the high half is a constant, and
+// the low half of another stage or K offset is this one plus (bytes >> 4) (shared memory addresses
+// stay below 2^18, so the address field never carries). Building each descriptor anew cost the one
+// thread that issues the MMAs some 880 cycles of dependent arithmetic per K-step of 8 MMAs.
+__device__ __forceinline__ uint32_t sw128_desc_lo(uint32_t saddr, uint32_t lbo) {
+  return ((saddr & 0x3FFFFu) >> 4) | (((lbo >> 4) & 0x3FFFu) << 16);
+}
+constexpr uint32_t kSw128DescHi = (1024u >> 4) | (1u << 14) | (2u << 29);   // SBO 1024
+__device__ __forceinline__ uint64_t sw128_desc_of(uint32_t lo) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(kSw128DescHi));
+  return d;
+}
+
 // Instruction descriptor, kind::f16: fp32 accumulator, bf16 A and B, M x N tile.
 __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, bool a_mn_major,
                                                   bool b_mn_major) {

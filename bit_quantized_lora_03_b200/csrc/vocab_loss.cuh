@@ -256,6 +256,8 @@ __global__ void __launch_bounds__(vg::kThreads, 1)
   } else if (warp == kMmaWarp) {
     if (lane == 0 && rank == 0) {
       constexpr uint32_t kIdesc = idesc_bf16(BM, BN, false, kBmn);
+      const uint32_t a_lo0 = sw128_desc_lo(smem_addr(smem), 16);
+      const uint32_t b_lo0 = sw128_desc_lo(smem_addr(smem) + A_BYTES, kBmn ? 8192 : 16);
       int g = 0, n = 0;
       bool ok = true;
       for (int item = pair; ok && item < args.items; item += pairs, ++n) {
@@ -268,16 +270,12 @@ __global__ void __launch_bounds__(vg::kThreads, 1)
           const uint32_t ph = (g / STAGES) & 1;
           if (!mbar_wait(&full[slot], ph, abort_flag)) { ok = false; break; }
           tc_fence_after();
+          const uint32_t a_lo = a_lo0 + slot * (STAGE_BYTES >> 4), b_lo = b_lo0 + slot * (STAGE_BYTES >> 4);
 #pragma unroll
-          for (int s = 0; s < KS; ++s) {
-            const uint32_t a_addr = smem_addr(smem + slot * STAGE_BYTES) + s * ATOM, b_addr = a_addr + A_BYTES;
-#pragma unroll
-            for (int kk = 0; kk < BK / 16; ++kk) {
-              const uint64_t ad = sw128_desc(a_addr + kk * 32, 16, 1024);
-              const uint64_t bd = kBmn ? sw128_desc(b_addr + kk * 2048, 8192, 1024)
-                                       : sw128_desc(b_addr + kk * 32, 16, 1024);
-              umma2_bf16(tmem_base + buf * BN, ad, bd, kIdesc, (kb > it.kb0 || s > 0 || kk > 0) ? 1u : 0u);
-            }
+          for (int k = 0; k < KS * (BK / 16); ++k) {
+            const uint32_t s = (k / (BK / 16)) * (ATOM >> 4), kk = k % (BK / 16);
+            umma2_bf16(tmem_base + buf * BN, sw128_desc_of(a_lo + s + kk * 2),
+                       sw128_desc_of(b_lo + s + kk * (kBmn ? 128 : 2)), kIdesc, (kb > it.kb0 || k > 0) ? 1u : 0u);
           }
           umma2_commit_multicast(&empty[slot], 0x3);   // frees the stage in both CTAs
         }
@@ -589,20 +587,21 @@ __device__ __forceinline__ bool narrow_mma(const NarrowCta& c, int n16, int buf,
   if (!mbar_wait(&c.acc_empty[buf], ((n >> 1) & 1) ^ 1u, c.abort_flag)) return false;
   tc_fence_after();
   const uint32_t idesc = idesc_bf16(vn::BM, n16, kAmn, false);
+  const uint32_t a_lo0 = sw128_desc_lo(smem_addr(c.stage), kAmn ? 8192 : 16);
+  const uint32_t b_lo0 = sw128_desc_lo(smem_addr(c.stage) + vn::A_BYTES, 16);
   for (int k = 0; k < steps; ++k, g.next(c.stages)) {
     const int slot = g.slot;
     if (!mbar_wait(&c.full[slot], g.phase, c.abort_flag)) return false;
     tc_fence_after();
+    const uint32_t a_lo = a_lo0 + slot * (c.stage_bytes >> 4), b_lo = b_lo0 + slot * (c.stage_bytes >> 4);
 #pragma unroll
-    for (int s = 0; s < vn::KS; ++s) {
-      const uint32_t a_addr = smem_addr(c.stage + slot * c.stage_bytes) + s * vn::A_ATOM;
-      const uint32_t b_addr = smem_addr(c.stage + slot * c.stage_bytes) + vn::A_BYTES + s * n16 * (vn::BK * 2);
+    for (int s = 0; s < vn::KS; ++s)
 #pragma unroll
       for (int kk = 0; kk < vn::BK / 16; ++kk)
         umma_bf16(c.tmem + buf * (c.tmem_cols / 2),
-                  kAmn ? sw128_desc(a_addr + kk * 2048, 8192, 1024) : sw128_desc(a_addr + kk * 32, 16, 1024),
-                  sw128_desc(b_addr + kk * 32, 16, 1024), idesc, (k > 0 || s > 0 || kk > 0) ? 1u : 0u);
-    }
+                  sw128_desc_of(a_lo + s * (vn::A_ATOM >> 4) + kk * (kAmn ? 128 : 2)),
+                  sw128_desc_of(b_lo + s * n16 * (vn::BK * 2 / 16) + kk * 2), idesc,
+                  (k > 0 || s > 0 || kk > 0) ? 1u : 0u);
     umma_commit(&c.empty[slot]);
   }
   umma_commit(&c.acc_full[buf]);
