@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(acc_full + 1);
   volatile uint32_t* abort_flag = tmem_holder + 1;
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform_warp(), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();             // 0: MMA issuer, 1: its peer
   // Grid x walks the column tiles (two CTAs each) and grid y the 512-token row blocks, so the
   // pairs resident at one time share a few row blocks of A (the larger operand) across all
@@ -239,7 +239,7 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
       }
     }
   } else if (warp == kMmaWarp) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
       // M = 256 per instruction (128 rows from each CTA), N = 256 (128 columns from each)
       constexpr uint32_t kIdescMain = idesc_bf16(256, BN, false, kBwd);
       constexpr uint32_t kIdescLora = idesc_bf16(256, BN, false, !kBwd);
@@ -249,8 +249,8 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
       for (int i = 0; i < total; ++i) {
         const int slot = i % STAGES;
         const uint32_t ph = (i / STAGES) & 1;
-        if (!mbar_wait(&full_a[slot], ph, abort_flag)) break;
-        if (!mbar_wait(&full_b[slot], ph, abort_flag)) break;
+        if (!mbar_wait_warp(&full_a[slot], ph, abort_flag)) break;
+        if (!mbar_wait_warp(&full_b[slot], ph, abort_flag)) break;
         tc_fence_after();
         // A is K-major; B (the weights forward, L1 backward) K-major or (L2 forward, the weights
         // backward) MN-major
@@ -265,16 +265,23 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
                          (i > 0 || kk > 0) ? 1u : 0u);
           }
         };
-        if ((i >= nk) == kBwd)
-          issue(b_lo_k + b_off, 2, i >= nk ? kIdescLora : kIdescMain);
-        else
-          issue(b_lo_mn + b_off, 128, i >= nk ? kIdescLora : kIdescMain);
-        umma2_commit_multicast(&empty[slot], 0x3);   // frees the stage in both CTAs
+        if (elect_one()) {
+          if ((i >= nk) == kBwd)
+            issue(b_lo_k + b_off, 2, i >= nk ? kIdescLora : kIdescMain);
+          else
+            issue(b_lo_mn + b_off, 128, i >= nk ? kIdescLora : kIdescMain);
+          umma2_commit_multicast(&empty[slot], 0x3);   // frees the stage in both CTAs
+        }
+        __syncwarp();
         any = true;
       }
       // completes in both CTAs once every MMA above has finished (also after an abort)
-      umma2_commit_multicast(acc_full, 0x3);
-      if (*abort_flag && any) mbar_drain(acc_full, 0);
+      // (elect picks the lane that issued them)
+      if (elect_one()) {
+        umma2_commit_multicast(acc_full, 0x3);
+        if (*abort_flag && any) mbar_drain(acc_full, 0);
+      }
+      __syncwarp();
     }
   } else {
     // ---------------- warps 0-7: dequant producers (a 64-weight block per thread per stage: 128
@@ -393,7 +400,7 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
     if (kEpi == kEpiFused && epi_row0 < args.M) epi_load(n0);
     const bool done = mbar_wait_warp(acc_full, 0, abort_flag);
     tc_fence_after();
-    if (__shfl_sync(0xFFFFFFFFu, done && !*abort_flag, 0)) {
+    if (__all_sync(0xFFFFFFFFu, done && !*abort_flag)) {
       if (args.addend) pdl_wait();
       const int acc = warp >> 2, quad = warp & 3;
       const int row0 = mrow + acc * 256 + quad * 32;

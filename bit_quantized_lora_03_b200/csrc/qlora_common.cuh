@@ -91,13 +91,25 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity,
   }
 }
 
-// mbar_wait for a whole warp: lane 0 polls (32 lanes polling one barrier take shared-memory
-// bandwidth from the tensor core's operand reads) and every lane gets its result, so that the
-// warp goes one way whatever it is.
+// The warp's index within its block as a value the compiler knows to be the same in all its lanes, and
+// one elected lane of a converged warp. MMAs take their operands in uniform registers: issued from
+// warp-uniform code they are there already, from a branch taken by `lane == 0` each is moved first
+// (a K-step's 4 to 8 MMAs took 640 cycles to issue that way, 215 this way).
+__device__ __forceinline__ int uniform_warp() { return __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0); }
+__device__ __forceinline__ bool elect_one() {
+  uint32_t yes;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(yes));
+  return yes != 0;
+}
+
+// mbar_wait for a whole warp, which goes one way whatever its lanes saw. (All lanes poll: one lane
+// polling and a shuffle of its result took longer.)
 __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, volatile uint32_t* abort_flag) {
-  bool ok = true;
-  if ((threadIdx.x & 31) == 0) ok = mbar_wait(bar, parity, abort_flag);
-  return __shfl_sync(0xFFFFFFFFu, ok, 0);
+  return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort_flag));
 }
 
 // ------------------------------------------------------------------------------------------

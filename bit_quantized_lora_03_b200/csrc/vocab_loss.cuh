@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(vg::kThreads, 1)
   volatile uint32_t* abort_flag = tmem_holder + 1;
 
   if (kMode == kVocabProb && args.redo && *args.redo == 0u) return;   // (the whole grid alike)
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform_warp(), lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_ctarank());   // 0: MMA issuer, 1: its peer
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(vg::kThreads, 1)
       }
     }
   } else if (warp == kMmaWarp) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
       constexpr uint32_t kIdesc = idesc_bf16(BM, BN, false, kBmn);
       const uint32_t a_lo0 = sw128_desc_lo(smem_addr(smem), 16);
       const uint32_t b_lo0 = sw128_desc_lo(smem_addr(smem) + A_BYTES, kBmn ? 8192 : 16);
@@ -263,26 +263,34 @@ __global__ void __launch_bounds__(vg::kThreads, 1)
       for (int item = pair; ok && item < args.items; item += pairs, ++n) {
         const VocabItem it = vocab_item(args, item);
         const int buf = n & 1;
-        if (!mbar_wait(&acc_empty[buf], ((n >> 1) & 1) ^ 1u, abort_flag)) break;
+        if (!mbar_wait_warp(&acc_empty[buf], ((n >> 1) & 1) ^ 1u, abort_flag)) break;
         tc_fence_after();
         for (int kb = it.kb0; kb < it.kb1; ++kb, ++g) {
           const int slot = g % STAGES;
           const uint32_t ph = (g / STAGES) & 1;
-          if (!mbar_wait(&full[slot], ph, abort_flag)) { ok = false; break; }
+          if (!mbar_wait_warp(&full[slot], ph, abort_flag)) { ok = false; break; }
           tc_fence_after();
           const uint32_t a_lo = a_lo0 + slot * (STAGE_BYTES >> 4), b_lo = b_lo0 + slot * (STAGE_BYTES >> 4);
+          if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < KS * (BK / 16); ++k) {
-            const uint32_t s = (k / (BK / 16)) * (ATOM >> 4), kk = k % (BK / 16);
-            umma2_bf16(tmem_base + buf * BN, sw128_desc_of(a_lo + s + kk * 2),
-                       sw128_desc_of(b_lo + s + kk * (kBmn ? 128 : 2)), kIdesc, (kb > it.kb0 || k > 0) ? 1u : 0u);
+            for (int k = 0; k < KS * (BK / 16); ++k) {
+              const uint32_t s = (k / (BK / 16)) * (ATOM >> 4), kk = k % (BK / 16);
+              umma2_bf16(tmem_base + buf * BN, sw128_desc_of(a_lo + s + kk * 2),
+                         sw128_desc_of(b_lo + s + kk * (kBmn ? 128 : 2)), kIdesc, (kb > it.kb0 || k > 0) ? 1u : 0u);
+            }
+            umma2_commit_multicast(&empty[slot], 0x3);   // frees the stage in both CTAs
           }
-          umma2_commit_multicast(&empty[slot], 0x3);   // frees the stage in both CTAs
+          __syncwarp();
         }
-        umma2_commit_multicast(&acc_full[buf], 0x3);
+        if (elect_one()) umma2_commit_multicast(&acc_full[buf], 0x3);
+        __syncwarp();
       }
-      umma2_commit_multicast(drained, 0x1);   // every MMA has read its operands before the CTAs leave
-      mbar_drain(drained, 0);
+      // every MMA has read its operands before the CTAs leave (elect picks the lane that issued them)
+      if (elect_one()) {
+        umma2_commit_multicast(drained, 0x1);
+        mbar_drain(drained, 0);
+      }
+      __syncwarp();
     }
   } else {
     // ---------------- epilogue: warp w has accumulator rows 32 w .. of this CTA, a row per lane ----
@@ -581,30 +589,34 @@ struct RingPos {
     }
   }
 };
-// The MMA thread's part of one accumulator: `steps` K-steps from the ring at position g.
+// The MMA warp's part of one accumulator: `steps` K-steps from the ring at position g.
 template <bool kAmn>
 __device__ __forceinline__ bool narrow_mma(const NarrowCta& c, int n16, int buf, int n, int steps, RingPos& g) {
-  if (!mbar_wait(&c.acc_empty[buf], ((n >> 1) & 1) ^ 1u, c.abort_flag)) return false;
+  if (!mbar_wait_warp(&c.acc_empty[buf], ((n >> 1) & 1) ^ 1u, c.abort_flag)) return false;
   tc_fence_after();
   const uint32_t idesc = idesc_bf16(vn::BM, n16, kAmn, false);
   const uint32_t a_lo0 = sw128_desc_lo(smem_addr(c.stage), kAmn ? 8192 : 16);
   const uint32_t b_lo0 = sw128_desc_lo(smem_addr(c.stage) + vn::A_BYTES, 16);
   for (int k = 0; k < steps; ++k, g.next(c.stages)) {
     const int slot = g.slot;
-    if (!mbar_wait(&c.full[slot], g.phase, c.abort_flag)) return false;
+    if (!mbar_wait_warp(&c.full[slot], g.phase, c.abort_flag)) return false;
     tc_fence_after();
     const uint32_t a_lo = a_lo0 + slot * (c.stage_bytes >> 4), b_lo = b_lo0 + slot * (c.stage_bytes >> 4);
+    if (elect_one()) {
 #pragma unroll
-    for (int s = 0; s < vn::KS; ++s)
+      for (int s = 0; s < vn::KS; ++s)
 #pragma unroll
-      for (int kk = 0; kk < vn::BK / 16; ++kk)
-        umma_bf16(c.tmem + buf * (c.tmem_cols / 2),
-                  sw128_desc_of(a_lo + s * (vn::A_ATOM >> 4) + kk * (kAmn ? 128 : 2)),
-                  sw128_desc_of(b_lo + s * n16 * (vn::BK * 2 / 16) + kk * 2), idesc,
-                  (k > 0 || s > 0 || kk > 0) ? 1u : 0u);
-    umma_commit(&c.empty[slot]);
+        for (int kk = 0; kk < vn::BK / 16; ++kk)
+          umma_bf16(c.tmem + buf * (c.tmem_cols / 2),
+                    sw128_desc_of(a_lo + s * (vn::A_ATOM >> 4) + kk * (kAmn ? 128 : 2)),
+                    sw128_desc_of(b_lo + s * n16 * (vn::BK * 2 / 16) + kk * 2), idesc,
+                    (k > 0 || s > 0 || kk > 0) ? 1u : 0u);
+      umma_commit(&c.empty[slot]);
+    }
+    __syncwarp();
   }
-  umma_commit(&c.acc_full[buf]);
+  if (elect_one()) umma_commit(&c.acc_full[buf]);
+  __syncwarp();
   return true;
 }
 // After an abort: no copy may still be writing shared memory, no MMA reading it, when the CTA exits.
@@ -625,7 +637,7 @@ __global__ void __launch_bounds__(vn::kThreads, 1)
   using namespace vn;
   extern __shared__ uint8_t smem_raw[];
   if (kMode == kVocabProb && args.redo && *args.redo == 0u) return;   // (the whole grid alike)
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform_warp(), lane = threadIdx.x & 31;
   NarrowCta cta = narrow_setup(smem_raw, args.n16);
   // per token: what the epilogue needs of it (a word that is nobody's target: -1)
   float *t_ref = cta.token, *t_a = cta.token + kMaxTokens, *t_b = cta.token + 2 * kMaxTokens;
@@ -672,15 +684,13 @@ __global__ void __launch_bounds__(vn::kThreads, 1)
       narrow_drain_copies(cta, g);
     }
   } else if (warp == kMmaWarp) {
-    if (lane == 0) {
-      RingPos g;
-      int n = 0;
-      // (a last tile of fewer than four units leaves the other rows of its operand as they were: their
-      // accumulator rows are not read)
-      for (int u = u0; u < u1; u += 4, ++n)
-        if (!narrow_mma<false>(cta, args.n16, n & 1, n, args.num_kb, g)) break;
-      narrow_drain_mma(cta, g);
-    }
+    RingPos g;
+    int n = 0;
+    // (a last tile of fewer than four units leaves the other rows of its operand as they were: their
+    // accumulator rows are not read)
+    for (int u = u0; u < u1; u += 4, ++n)
+      if (!narrow_mma<false>(cta, args.n16, n & 1, n, args.num_kb, g)) break;
+    narrow_drain_mma(cta, g);
   } else {
     int n = 0;
     for (int u = u0; u < u1; u += 4, ++n) {
@@ -763,7 +773,7 @@ __global__ void __launch_bounds__(vn::kThreads, 1)
                              const VocabNarrowArgs args) {
   using namespace vn;
   extern __shared__ uint8_t smem_raw[];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform_warp(), lane = threadIdx.x & 31;
   NarrowCta cta = narrow_setup(smem_raw, args.n16);
   narrow_begin(cta);
   const int total = args.tiles * args.num_kb;
@@ -794,13 +804,11 @@ __global__ void __launch_bounds__(vn::kThreads, 1)
       narrow_drain_copies(cta, g);
     }
   } else if (warp == kMmaWarp) {
-    if (lane == 0) {
-      RingPos g;
-      int n = 0;
-      for (int x = x0; x < x1; x = share_end(x), ++n)
-        if (!narrow_mma<true>(cta, args.n16, n & 1, n, share_end(x) - x, g)) break;
-      narrow_drain_mma(cta, g);
-    }
+    RingPos g;
+    int n = 0;
+    for (int x = x0; x < x1; x = share_end(x), ++n)
+      if (!narrow_mma<true>(cta, args.n16, n & 1, n, share_end(x) - x, g)) break;
+    narrow_drain_mma(cta, g);
   } else {
     int n = 0;
     for (int x = x0; x < x1; x = share_end(x), ++n) {
