@@ -438,19 +438,19 @@ GemvWs carve_gemv(void* base, int64_t t, int64_t o, int64_t r) {
 constexpr int64_t kGemvMaxTokens = 16;
 
 // Shares of K of the linear with the fused epilogue (t > kGemvMaxTokens): its tiles of 512 tokens x 256
-// outputs leave most of the card idle for a few hundred tokens. A K-step takes about 0.75 us (0.45 with
-// one accumulator), a round of pairs as long as a tile's share; the shares cost their fp32 traffic at some
-// 5 TB/s and another launch. 4096 -> 4096: 17 tokens 64 -> 22 us;
-// 11008 -> 4096: 777 tokens 150 -> 93 us.
+// outputs leave most of the card idle for a few hundred tokens. A K-step takes about 0.6 us (0.47 with
+// one accumulator) and a share 11 us (7) besides, a round of pairs as long as one share; the shares cost
+// their fp32 traffic at some 5 TB/s and another launch. 4096 -> 4096: 17 tokens 64 -> 18 us with the join;
+// 11008 -> 4096: 777 tokens 150 -> 83 us.
 int epilogue_shares(int64_t t, int64_t h, int64_t o, int sms) {
   const int64_t tiles = (t + 511) / 512 * ((o + 255) / 256), kb = h / 64, pairs = sms / 2;
-  const double step = t > 256 ? 0.75 : 0.45;
+  const double step = t > 256 ? 0.6 : 0.47, fixed = t > 256 ? 11.0 : 7.0;
   int best = 1;
   double cost = 0.0;
   for (int s = 1; s <= 16 && kb / s >= 4; ++s) {
     const int64_t per = (kb + s - 1) / s;
     if (s > 1 && per * (s - 1) >= kb) continue;   // a share would be empty
-    const double c = static_cast<double>((tiles * s + pairs - 1) / pairs) * (per * step + 5.0) +
+    const double c = static_cast<double>((tiles * s + pairs - 1) / pairs) * (per * step + fixed) +
                      (s > 1 ? 8.0 * s * t * o / 5e6 + 4.0 : 0.0);
     if (s == 1 || c < cost) {
       cost = c;

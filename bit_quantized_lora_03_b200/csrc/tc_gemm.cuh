@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(tcg::kThreads, kMinCtas)
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(acc_full + 1);
   volatile uint32_t* abort_flag = tmem_holder + 1;
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = uniform_warp(), lane = threadIdx.x & 31;
   const int m0 = blockIdx.y * BM;
   const int nb0 = blockIdx.x * BNp;  // this CTA's first output column (N tiles along grid x)
   const int kb0 = blockIdx.z * args.kb_per_split;
@@ -154,10 +154,9 @@ __global__ void __launch_bounds__(tcg::kThreads, kMinCtas)
   if (warp == kTmaWarp) {
     if (lane == 0) {
       if (args.pdl == kPdlWaitFirst) pdl_wait();  // every global access follows the loads
-      int issued = 0;
+      int issued = 0, slot = 0;
+      uint32_t ph = 0;
       for (int i = 0; i < nk; ++i) {
-        const int slot = i % STAGES;
-        const uint32_t ph = (i / STAGES) & 1;
         if (!mbar_wait(&empty[slot], ph ^ 1u, abort_flag)) break;
         const int kb = kb0 + i;
         mbar_arrive_expect_tx(&full[slot], A_BYTES + bbytes);
@@ -177,6 +176,10 @@ __global__ void __launch_bounds__(tcg::kThreads, kMinCtas)
         }
         if (i == 0) QLORA_STAMP(2);
         issued = i + 1;
+        if (++slot == STAGES) {
+          slot = 0;
+          ph ^= 1u;
+        }
       }
       if (*abort_flag) {
         for (int j = (issued > STAGES ? issued - STAGES : 0); j < issued; ++j)
@@ -184,32 +187,40 @@ __global__ void __launch_bounds__(tcg::kThreads, kMinCtas)
       }
     }
   } else if (warp == kMmaWarp) {
-    if (lane == 0) {
-      const uint32_t idesc = idesc_bf16(BM, BNp, A_MN, B_MN);
-      bool any = false;
-      for (int i = 0; i < nk; ++i) {
-        const int slot = i % STAGES;
-        const uint32_t ph = (i / STAGES) & 1;
-        if (!mbar_wait(&full[slot], ph, abort_flag)) break;
+    const uint32_t idesc = idesc_bf16(BM, BNp, A_MN, B_MN);
+    const uint32_t a_lo0 = sw128_desc_lo(smem_addr(smem), A_MN ? 8192 : 16);
+    const uint32_t b_lo0 = sw128_desc_lo(smem_addr(smem) + A_BYTES, B_MN ? 8192 : 16);
+    bool any = false;
+    int slot = 0;          // i % STAGES and its parity, counted: STAGES is known at run time only
+    uint32_t ph = 0;
+    for (int i = 0; i < nk; ++i) {
+      if (!mbar_wait_warp(&full[slot], ph, abort_flag)) break;
+      if (lane == 0) {
         if (i == 0) QLORA_STAMP(3);
         if (i == nk - 1) QLORA_STAMP(4);
-        tc_fence_after();
-        const uint32_t a_addr = smem_addr(smem + slot * SB);
-        const uint32_t b_addr = a_addr + A_BYTES;
-#pragma unroll
-        for (int kk = 0; kk < BK / 16; ++kk) {
-          const uint64_t ad = A_MN ? sw128_desc(a_addr + kk * 2048, 8192, 1024)
-                                   : sw128_desc(a_addr + kk * 32, 16, 1024);
-          const uint64_t bd = B_MN ? sw128_desc(b_addr + kk * 2048, 8192, 1024)
-                                   : sw128_desc(b_addr + kk * 32, 16, 1024);
-          umma_bf16(tmem_base, ad, bd, idesc, (i > 0 || kk > 0) ? 1u : 0u);
-        }
-        umma_commit(&empty[slot]);
-        any = true;
       }
+      tc_fence_after();
+      const uint32_t off = slot * (static_cast<uint32_t>(SB) >> 4);
+      if (elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < BK / 16; ++kk)
+          umma_bf16(tmem_base, sw128_desc_of(a_lo0 + off + kk * (A_MN ? 128 : 2)),
+                    sw128_desc_of(b_lo0 + off + kk * (B_MN ? 128 : 2)), idesc, (i > 0 || kk > 0) ? 1u : 0u);
+        umma_commit(&empty[slot]);
+      }
+      __syncwarp();
+      any = true;
+      if (++slot == STAGES) {
+        slot = 0;
+        ph ^= 1u;
+      }
+    }
+    // (elect picks the lane that issued them)
+    if (elect_one()) {
       umma_commit(acc_full);
       if (*abort_flag && any) mbar_drain(acc_full, 0);
     }
+    __syncwarp();
   } else {
     // ---------------- epilogue warps 0-3: one accumulator row per thread ------------------
     const bool ok = (nk > 0) && mbar_wait(acc_full, 0, abort_flag);
