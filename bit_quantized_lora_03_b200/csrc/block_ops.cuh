@@ -389,11 +389,9 @@ int qlora_linear_fwd_epilogue(const uint16_t* X, int64_t t, const nf4_weight* W,
 
 size_t qlora_fwd_epilogue_workspace_bytes(int64_t t, int64_t h, int64_t o, int64_t r) {
   const size_t base = qlora_fwd_workspace_bytes(t, h, o, r);
-  if (!base || t <= kGemvMaxTokens) return base;
-  // (the shares of a call depend on the card's size: the most any B200 takes)
-  int most = 1;
-  for (int sms = 100; sms <= kMaxSms; ++sms) most = std::max(most, epilogue_shares(t, h, o, sms));
-  return base + (most > 1 ? static_cast<size_t>(most) * t * o * 4 : 0);
+  if (!base || !epilogue_uses_gemm(t, h, o)) return base;
+  const int shares = epilogue_shares(t, h, o);
+  return lora_region_bytes(t, r) + (shares > 1 ? static_cast<size_t>(shares) * t * o * 4 : 0);
 }
 
 size_t qlora_epilogue_bwd_workspace_bytes(int64_t t, int64_t o) {

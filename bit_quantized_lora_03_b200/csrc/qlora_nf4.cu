@@ -437,13 +437,13 @@ GemvWs carve_gemv(void* base, int64_t t, int64_t o, int64_t r) {
 
 constexpr int64_t kGemvMaxTokens = 16;
 
-// Shares of K of the linear with the fused epilogue (t > kGemvMaxTokens): its tiles of 512 tokens x 256
+// Shares of K of the linear with the fused epilogue on the tcgen05 path: its tiles of 512 tokens x 256
 // outputs leave most of the card idle for a few hundred tokens. A K-step takes about 0.6 us (0.47 with
 // one accumulator) and a share 11 us (7) besides, a round of pairs as long as one share; the shares cost
 // their fp32 traffic at some 5 TB/s and another launch. 4096 -> 4096: 17 tokens 64 -> 18 us with the join;
-// 11008 -> 4096: 777 tokens 150 -> 83 us.
-int epilogue_shares(int64_t t, int64_t h, int64_t o, int sms) {
-  const int64_t tiles = (t + 511) / 512 * ((o + 255) / 256), kb = h / 64, pairs = sms / 2;
+// 11008 -> 4096: 777 tokens 150 -> 83 us. Planned for 148 SMs, so that the workspace is a host function.
+int epilogue_shares(int64_t t, int64_t h, int64_t o) {
+  const int64_t tiles = (t + 511) / 512 * ((o + 255) / 256), kb = h / 64, pairs = 148 / 2;
   const double step = t > 256 ? 0.6 : 0.47, fixed = t > 256 ? 11.0 : 7.0;
   int best = 1;
   double cost = 0.0;
@@ -458,6 +458,14 @@ int epilogue_shares(int64_t t, int64_t h, int64_t o, int sms) {
     }
   }
   return best;
+}
+
+// Whether the linear with the fused epilogue takes the tcgen05 path: above the GEMV's tokens, and from 9
+// tokens (the GEMV's second token tile) where the weight is large and its shares fill the card. 16 tokens,
+// 8192 -> 8192: GEMV 63 us, this 42; 11008 -> 4096: 58 and 33; 2048 -> 8192: 36 and 22; with one share
+// 4096 -> 11008: 41 and 46.
+bool epilogue_uses_gemm(int64_t t, int64_t h, int64_t o) {
+  return t > kGemvMaxTokens || (t > 8 && h * o >= (int64_t(1) << 23) && epilogue_shares(t, h, o) > 1);
 }
 
 // ------------------------------------------------------------------------------------------
@@ -731,7 +739,7 @@ int fwd_core(const uint16_t* X, const uint16_t* Xl, int64_t t, const nf4_weight*
   if ((rc = current_device(&dev))) return rc;
   const int64_t h = W->in_features, o = W->out_features;
   const int sms = sm_count(dev);
-  if (t <= kGemvMaxTokens) {
+  if (epi ? !epilogue_uses_gemm(t, h, o) : t <= kGemvMaxTokens) {
     // partial sums of Xl.L1 (+ zeroed sums and counters), then the GEMV, which forms
     // sT = bf16(s . Xl.L1) and finishes Y
     GemvWs gw = carve_gemv(workspace, t, o, r);
@@ -819,7 +827,7 @@ int fwd_core(const uint16_t* X, const uint16_t* Xl, int64_t t, const nf4_weight*
   ga.tab = device_table();
   if (epi) {
     ga.epi = *epi;
-    const int shares = epilogue_shares(t, h, o, sms);
+    const int shares = epilogue_shares(t, h, o);
     if (shares == 1) return launch_nf4_gemm<false, kEpiFused>(mA, mP, mA2, mB2, ga, t, o, st, prof::kGemmFwd);
     float* part = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(workspace) + lora_region_bytes(t, r));
     ga.kb_per_split = (ga.num_kb + shares - 1) / shares;
