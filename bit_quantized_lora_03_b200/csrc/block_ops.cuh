@@ -14,12 +14,12 @@ bool valid_act(int act) { return act >= QLORA_ACT_NONE && act <= QLORA_ACT_SILU;
 static_assert(kActNone == QLORA_ACT_NONE && kActRelu == QLORA_ACT_RELU && kActGelu == QLORA_ACT_GELU &&
               kActGeluTanh == QLORA_ACT_GELU_TANH && kActSilu == QLORA_ACT_SILU, "activation ids");
 
-// Runs of rows of the epilogue's backward: one wave of CTAs over the card, each with at least two
+// Runs of rows of the epilogue's backward: one wave of CTAs over the card, each with at least four
 // rounds of its warps' rows in flight, so that a short batch is not cut into runs whose partial sums
 // cost more than they save. The workspace is sized for the most runs there can be (sms = 0).
 constexpr int kMaxEpiRuns = 1024;
 int epilogue_runs(int64_t t, int64_t o, int sms, int ctas) {
-  const int64_t rows = 2 * ep::kUnroll * ep::kWarps;
+  const int64_t rows = 4 * ep::kUnroll * ep::kWarps;
   int64_t runs = std::min<int64_t>((t + rows - 1) / rows, kMaxEpiRuns);
   const int64_t blocks = (o + ep::kCols - 1) / ep::kCols;
   if (sms) runs = std::min(runs, std::max<int64_t>(1, static_cast<int64_t>(sms) * ctas / blocks));
