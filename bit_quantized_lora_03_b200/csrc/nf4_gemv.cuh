@@ -288,26 +288,34 @@ template <int NT, bool kEpi>
 __device__ __forceinline__ void gemv_finish_tile(const GemvArgs& a, const uint16_t* sts,
                                                  int64_t tile, int lane) {
   const int64_t row = tile * gv::kTileRows + lane;
+  // the operands that do not depend on the sums go in flight with them: one latency, not three
+  float l2[8];
+  auto load_l2 = [&](int c0) {   // r % 16 == 0: eight loads in flight per lane
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      l2[j] = bf16_bits_to_float(__ldg(a.L2 + static_cast<int64_t>(c0 + j) * a.o + row));
+  };
+  load_l2(0);
+  const float bias = kEpi && a.epi.bias ? bf16_bits_to_float(__ldg(a.epi.bias + row)) : 0.f;
   float y[NT * 8];
 #pragma unroll
   for (int n = 0; n < NT * 8; ++n)
     y[n] = n < a.t ? __ldcg(a.Y32 + static_cast<int64_t>(n) * a.o + row) : 0.f;
-  for (int c0 = 0; c0 < a.r; c0 += 8) {  // r % 16 == 0: eight loads in flight per lane
-    float l2[8];
+  for (int c0 = 0; c0 < a.r; c0 += 8) {
+    float cur[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      l2[j] = bf16_bits_to_float(__ldg(a.L2 + static_cast<int64_t>(c0 + j) * a.o + row));
+    for (int j = 0; j < 8; ++j) cur[j] = l2[j];
+    if (c0 + 8 < a.r) load_l2(c0 + 8);
 #pragma unroll
     for (int j = 0; j < 8; ++j)
 #pragma unroll
       for (int n = 0; n < NT * 8; ++n)
-        if (n < a.t) y[n] = fmaf(bf16_bits_to_float(sts[n * gv::kMaxRank + c0 + j]), l2[j], y[n]);
+        if (n < a.t) y[n] = fmaf(bf16_bits_to_float(sts[n * gv::kMaxRank + c0 + j]), cur[j], y[n]);
   }
   if (kEpi) {   // Z = y + b, Y = act(Z) + R; lane = row of Wt: 64-byte pieces of a token's row
-    const float b = a.epi.bias ? bf16_bits_to_float(__ldg(a.epi.bias + row)) : 0.f;
 #pragma unroll
     for (int n = 0; n < NT * 8; ++n) {
-      y[n] += b;
+      y[n] += bias;
       if (n < a.t && a.epi.z_out)
         a.epi.z_out[static_cast<int64_t>(n) * a.o + row] = __bfloat16_as_ushort(__float2bfloat16_rn(y[n]));
     }
@@ -385,10 +393,22 @@ __global__ void __launch_bounds__(gv::kThreads, 1)
   uint4 xc[NT][4], xn[NT][4];
   if (NT == 1 && kXAhead && nrun > 0) gemv_load_x<NT>(xc, args, cur.u0, g, q, 2 * cur.u0 + (q >> 1) < nblk);
 
+  // what finishing this run's first row tile will read, brought into L2 meanwhile
+  if (nrun > 0)
+    for (int c = lane; c < args.r; c += 32)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(args.L2 + static_cast<int64_t>(c) * args.o + cur.tile * kTileRows));
+
   if (threadIdx.x == 0) abort_flag = 0u;
-  for (int i = threadIdx.x; i < 256 * 32; i += kThreads) {
-    const int e = i >> 5;
-    table[i] = make_float2(args.tab.level[e >> 4], args.tab.level[e & 15]);
+  if (kWarps == 16) {
+    // entry 16 j + warp, this lane's copy: one dynamic index into the levels, not two per entry
+    const float lo = args.tab.level[warp];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) table[(16 * j + warp) * 32 + lane] = make_float2(args.tab.level[j], lo);
+  } else {
+    for (int i = threadIdx.x; i < 256 * 32; i += kThreads) {
+      const int e = i >> 5;
+      table[i] = make_float2(args.tab.level[e >> 4], args.tab.level[e & 15]);
+    }
   }
   // sT = bf16(s . X.L1) from the LoRA-down kernel's partial sums, once per CTA, by all its warps.
   // That kernel is launched just before this one, which may start early: wait for its completion
