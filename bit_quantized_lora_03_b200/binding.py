@@ -449,10 +449,13 @@ def _on(dev, t: torch.Tensor | None, dtype, shape, name: str) -> int | None:
     return t.data_ptr()
 
 
-def _out(dev, t: torch.Tensor | None, dtype, shape, name: str, want: bool = True):
-    """An output: t, checked, or a new tensor where one is wanted."""
+def _out(dev, t: torch.Tensor | None, dtype, shape, name: str, want: bool = True, like: torch.Tensor | None = None):
+    """An output: t, checked, or a new tensor where one is wanted (the quicker way where a checked
+    tensor of its type and shape is at hand: `like`)."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=dev) if want else None
+        if not want:
+            return None
+        return torch.empty(shape, dtype=dtype, device=dev) if like is None else torch.empty_like(like)
     _on(dev, t, dtype, shape, name)
     return t
 
@@ -504,7 +507,7 @@ def qlora_linear_fwd_epilogue(X: torch.Tensor, p: PackedNF4, L1: torch.Tensor, L
                _on(dev, L2, bf16, (r, o), "L2"), _on(dev, bias, bf16, (o,), "bias"),
                _on(dev, residual, bf16, (t, o), "residual"))
         Y = _out(dev, Y, bf16, (t, o), "Y")
-        Z = _out(dev, Z, bf16, (t, o), "Z", want_Z)
+        Z = _out(dev, Z, bf16, (t, o), "Z", want_Z, like=Y)
         sT = _out(dev, sT, bf16, (t, r), "sT", want_sT)
         ws = _scratch(dev, ws, int(lib().qlora_fwd_epilogue_workspace_bytes(t, h, o, r)))
         d = p.desc()
@@ -524,7 +527,7 @@ def qlora_epilogue_bwd(dY: torch.Tensor, Z: torch.Tensor | None, act="none",
     (t, o), dev = _matrix(dY, "dY"), dY.device
     with _guard(dY, stream):
         a, z = (_on(dev, x, torch.bfloat16, (t, o), n) for x, n in ((dY, "dY"), (Z, "Z")))
-        dZ = _out(dev, dZ, torch.bfloat16, (t, o), "dZ", want_dZ)
+        dZ = _out(dev, dZ, torch.bfloat16, (t, o), "dZ", want_dZ, like=dY)
         dbias = _out(dev, dbias, torch.float32, (o,), "dbias", want_dbias)
         if dbias is not None:
             ws = _scratch(dev, ws, int(lib().qlora_epilogue_bwd_workspace_bytes(t, o)))
@@ -556,8 +559,8 @@ def qlora_norm_residual_fwd(x: torch.Tensor, y: torch.Tensor | None = None,
         xp, yp = _on(dev, x, bf16, (t, h), "x"), _on(dev, y, bf16, (t, h), "y")
         wo, gp = _on(dev, w_post, bf16, (h,), "w_post"), _on(dev, gate, bf16, gshape, "gate")
         wi = _on(dev, w_pre, bf16, (h,), "w_pre")
-        x_out = _out(dev, x_out, bf16, (t, h), "x_out")
-        n = _out(dev, n, bf16, (t, h), "n", w_pre is not None)
+        x_out = _out(dev, x_out, bf16, (t, h), "x_out", like=x)
+        n = _out(dev, n, bf16, (t, h), "n", wi is not None, like=x)
         ro = torch.empty(t, dtype=torch.float32, device=dev) if want_rstd and wo else None
         ri = torch.empty(t, dtype=torch.float32, device=dev) if want_rstd and wi else None
         _check(lib().qlora_norm_residual_fwd(xp, yp, t, h, wo, gp, rows, float(scale), wi, float(eps),
@@ -589,8 +592,8 @@ def qlora_norm_residual_bwd(dx_out: torch.Tensor | None, dn: torch.Tensor | None
         wo, gp = _on(dev, w_post, bf16, (h,), "w_post"), _on(dev, gate, bf16, gshape, "gate")
         wi = _on(dev, w_pre_used, bf16, (h,), "w_pre")
         ro, ri = _on(dev, rstd_post, f32, (t,), "rstd_post"), _on(dev, rstd_pre, f32, (t,), "rstd_pre")
-        dx = torch.empty(t, h, dtype=bf16, device=dev)
-        dy = torch.empty(t, h, dtype=bf16, device=dev) if y is not None else None
+        dx = torch.empty_like(like)
+        dy = torch.empty_like(y) if y is not None else None
         dwo = torch.empty(h, dtype=f32, device=dev) if wo else None
         dg = torch.empty(gshape, dtype=f32, device=dev) if gp else None
         dwi = torch.empty(h, dtype=f32, device=dev) if wi else None
@@ -619,7 +622,8 @@ def qlora_vocab_loss_fwd(X: torch.Tensor, W: torch.Tensor, targets: torch.Tensor
     with _guard(X, stream):
         (t, h, v), args = _vocab(X, W, targets)
         dev, f32 = X.device, torch.float32
-        loss, lse = _out(dev, loss, f32, (t,), "loss"), _out(dev, lse, f32, (t,), "lse")
+        loss = _out(dev, loss, f32, (t,), "loss")
+        lse = _out(dev, lse, f32, (t,), "lse", like=loss)
         ws = _scratch(dev, ws, int(lib().qlora_vocab_loss_fwd_workspace_bytes(t, h, v)))
         _check(lib().qlora_vocab_loss_fwd(*args, int(ignore_index), loss.data_ptr(), lse.data_ptr(),
                                           ws.data_ptr(), ws.numel(), _current(dev)), "qlora_vocab_loss_fwd")
@@ -635,7 +639,7 @@ def qlora_vocab_loss_bwd(X: torch.Tensor, W: torch.Tensor, targets: torch.Tensor
         (t, h, v), args = _vocab(X, W, targets)
         dev, f32 = X.device, torch.float32
         grads = (_on(dev, lse, f32, (t,), "lse"), _on(dev, dloss, f32, (t,), "dloss"), _on(dev, dlse, f32, (t,), "dlse"))
-        dX = _out(dev, dX, torch.bfloat16, (t, h), "dX")
+        dX = _out(dev, dX, torch.bfloat16, (t, h), "dX", like=X)
         ws = _scratch(dev, ws, int(lib().qlora_vocab_loss_bwd_workspace_bytes(t, h, v)))
         _check(lib().qlora_vocab_loss_bwd(*args, int(ignore_index), *grads, dX.data_ptr(), ws.data_ptr(),
                                           ws.numel(), _current(dev)), "qlora_vocab_loss_bwd")
@@ -652,8 +656,9 @@ def qlora_vocab_loss_fwd_bwd(X: torch.Tensor, W: torch.Tensor, targets: torch.Te
         (t, h, v), args = _vocab(X, W, targets)
         dev, f32 = X.device, torch.float32
         d = _on(dev, dloss, f32, (t,), "dloss")
-        loss, lse = _out(dev, loss, f32, (t,), "loss"), _out(dev, lse, f32, (t,), "lse")
-        dX = _out(dev, dX, torch.bfloat16, (t, h), "dX")
+        loss = _out(dev, loss, f32, (t,), "loss")
+        lse = _out(dev, lse, f32, (t,), "lse", like=loss)
+        dX = _out(dev, dX, torch.bfloat16, (t, h), "dX", like=X)
         ws = _scratch(dev, ws, int(lib().qlora_vocab_loss_fwd_bwd_workspace_bytes(t, h, v)))
         _check(lib().qlora_vocab_loss_fwd_bwd(*args, int(ignore_index), d, loss.data_ptr(), lse.data_ptr(),
                                               dX.data_ptr(), ws.data_ptr(), ws.numel(), _current(dev)),
