@@ -79,22 +79,22 @@ constexpr int kVocabMaxParts = kMaxSms;   // partial tiles of a split K
 
 // Up to this many tokens go through the kernels that stream W past them (one 256-token tile of the
 // others is computed whole whatever it holds). Measured on 32000 x 4096, loss and
-// gradient: 104 us at 16 tokens, 111 at 64, 125 at 128, against 123 for any number up to 256.
-constexpr int64_t kVocabNarrowTokens = 112;
+// gradient: 106 us at 16 tokens, 116 at 64, 123 at 80, against 131 for any number up to 256.
+constexpr int64_t kVocabNarrowTokens = vn::kMaxTokens;
 constexpr int64_t kFewRows = 1024;   // rows that get a CTA each in the kernels over rows (a warp each above)
 
 struct VocabPlan {
   bool narrow;
   int64_t run;      // tokens per run
   int64_t ldp;      // v rounded up to 64
-  int64_t n_tiles;  // pieces of the vocabulary
+  int64_t pieces;   // of the vocabulary
   size_t g_bytes, stats_bytes, row_bytes, part_bytes;   // row_bytes: one float per token of a run
 };
 VocabPlan plan_vocab(int64_t t, int64_t h, int64_t v, bool stats, bool grad) {
   VocabPlan p{};
   p.narrow = t <= kVocabNarrowTokens;
   p.ldp = (v + 63) / 64 * 64;
-  p.n_tiles = p.narrow ? p.ldp / vn::kUnit : (v + vg::BN - 1) / vg::BN;
+  p.pieces = p.narrow ? p.ldp / vn::kUnit : (v + vg::BN - 1) / vg::BN * (vg::BN / vg::PIECE);
   const int64_t fit = static_cast<int64_t>(kVocabRunBytes / (static_cast<size_t>(p.ldp) * 2));
   p.run = grad ? std::min<int64_t>(t, std::max<int64_t>(vg::BM, fit / vg::BM * vg::BM)) : t;
   if (grad) {
@@ -104,7 +104,7 @@ VocabPlan plan_vocab(int64_t t, int64_t h, int64_t v, bool stats, bool grad) {
                             : static_cast<size_t>(kVocabMaxParts) * vg::BM * vg::BN * 4;
   }
   if (stats) {
-    p.stats_bytes = align256(static_cast<size_t>(p.run) * p.n_tiles * 8);
+    p.stats_bytes = align256(static_cast<size_t>(p.run) * p.pieces * 8);
     p.row_bytes = align256(static_cast<size_t>(p.run) * 4);
   }
   return p;
@@ -119,7 +119,7 @@ int check_vocab_shape(int64_t t, int64_t h, int64_t v) {
 size_t vocab_ws_bytes(int64_t t, int64_t h, int64_t v, bool stats, bool grad) {
   if (check_vocab_shape(t, h, v) != QLORA_OK) return 0;
   const VocabPlan p = plan_vocab(t, h, v, stats, grad);
-  return p.g_bytes + p.part_bytes + p.stats_bytes + 3 * p.row_bytes + 256;
+  return p.g_bytes + p.part_bytes + p.stats_bytes + 4 * p.row_bytes + 256;
 }
 
 // Tiles, their order and their split. Pairs walk the list in steps; row tiles are walked in groups
@@ -212,24 +212,26 @@ int vocab_core(const VocabCall& c, void* workspace, cudaStream_t st) {
   float* tl = reinterpret_cast<float*>(rows);
   float* factor = reinterpret_cast<float*>(rows + p.row_bytes);
   float* target_factor = reinterpret_cast<float*>(rows + 2 * p.row_bytes);
-  unsigned* redo = reinterpret_cast<unsigned*>(rows + 3 * p.row_bytes);
+  float* ref = reinterpret_cast<float*>(rows + 3 * p.row_bytes);
+  unsigned* redo = reinterpret_cast<unsigned*>(rows + 4 * p.row_bytes);
   const auto run_targets = [&](int64_t i0, int64_t n) {
     prof::Scope ps(prof::kVocabRows, st);
     const bool few = n <= kFewRows;
     (few ? vocab_target_kernel<8> : vocab_target_kernel<1>)<<<static_cast<unsigned>(few ? n : (n + 7) / 8), 256, 0, st>>>(
         c.X + i0 * c.h, c.W, c.targets + i0, c.ignore, static_cast<int>(n), static_cast<int>(c.h),
-        static_cast<int>(c.v), tl, redo);
+        static_cast<int>(c.v), ref, redo);
     return launch_status();
   };
   const auto run_rows = [&](int64_t i0, int64_t n) {
     VocabRowArgs r{};
     r.stats = st2;
     r.target_logit = tl;
+    r.ref = ref;
     r.targets = c.targets + i0;
     r.ignore = c.ignore;
     r.t = static_cast<int>(n);
     r.v = static_cast<int>(c.v);
-    r.pieces = static_cast<int>(p.n_tiles);
+    r.pieces = static_cast<int>(p.pieces);
     r.loss = c.loss + i0;
     r.lse = c.lse + i0;
     if (grad) {
@@ -255,6 +257,7 @@ int vocab_core(const VocabCall& c, void* workspace, cudaStream_t st) {
     a.ignore = c.ignore;
     a.stats = st2;
     a.target_logit = tl;
+    a.ref = ref;
     a.lse = c.lse;
     a.dloss = c.dloss;
     a.dlse = c.dlse;
@@ -316,6 +319,7 @@ int vocab_core(const VocabCall& c, void* workspace, cudaStream_t st) {
     a.ignore = c.ignore;
     a.stats = st2;
     a.target_logit = tl;
+    a.ref = ref;
     a.lse = c.lse + i0;
     if (grad) {
       a.dloss = c.dloss + i0;

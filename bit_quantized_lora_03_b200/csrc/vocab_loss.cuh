@@ -5,7 +5,7 @@
 //   b_i   = dloss_i (0 where y_i is not counted),  a_i = b_i + dlse_i.
 //
 // vocab_gemm_kernel is one persistent tcgen05 GEMM with four epilogues. The vocabulary is walked in
-// pieces of 256 columns: a CTA pair computes 256 tokens x 256 columns of logits into tensor memory
+// pieces of 128 columns: a CTA pair computes 256 tokens x 256 columns of logits into tensor memory
 // (fp32) and its epilogue reduces them there:
 //   kVocabStats   a token's reference point (its maximum) and sum of exp(l - reference) over the piece,
 //                 and the target's logit
@@ -26,10 +26,15 @@
 // sums overflow: the piece then raises a flag, and kVocabProb runs again over the run with its lse
 // (otherwise that launch returns at once).
 //
+// Logits are accumulated 512 inputs at a time in tensor memory and summed in the epilogue's registers.
+// The tensor core truncates its fp32 sum after every 16 inputs: over 4096 (8192) inputs a logit then
+// comes out 5e-6 (1.1e-5) of itself too small, which the loss, an fp32 value, would show; by pieces of
+// 512 it is 6e-7. g is rounded to bf16 anyway, and the second product accumulates as it comes.
+//
 // Bound: the tensor cores (2thv per product) for more than a few hundred tokens, reading W for few.
 // The design follows from the first: cta_group::2 (256 x 256 x 16 per instruction, each CTA loading
 // half of A and half of B), a six-stage TMA ring, and two accumulators in tensor memory, so that a
-// tile's epilogue (four warps) runs under the next tile's products. g is rounded to bf16 because it
+// tile's epilogue (eight warps) runs under the next tile's products. g is rounded to bf16 because it
 // is an operand of a bf16 product: a relative 2^-9 per term, against the 2^-9 of dX's own rounding.
 //
 // Every wait is bounded (qlora::mbar_wait); on expiry the CTA reports QLORA_DEV_TIMEOUT, stops
@@ -47,10 +52,13 @@ constexpr int STAGES = 3;
 constexpr int ATOM = 128 * BK * 2;           // this CTA's half of A, or of B, for one step
 constexpr int A_BYTES = KS * ATOM;
 constexpr int STAGE_BYTES = 2 * A_BYTES;
-constexpr int kEpiWarps = 4;
-constexpr int kTmaWarp = 4, kMmaWarp = 5;
-constexpr int kThreads = 6 * 32;
-constexpr int kStaging = kEpiWarps * 2 * 4096;   // two 32-row x 128-byte tiles per epilogue warp
+constexpr int CHUNK = 4;                     // stages per accumulation of logits (K = 512); a tile's first
+                                             // takes twice that, while the tile before is finished
+constexpr int PIECE = 128;                   // columns of a tile that one epilogue warp reduces
+constexpr int kEpiWarps = 8;                 // four for each half of a tile's columns
+constexpr int kTmaWarp = 8, kMmaWarp = 9;
+constexpr int kThreads = 10 * 32;
+constexpr int kStaging = kEpiWarps * 4096;   // a 32-row x 128-byte tile per epilogue warp
 constexpr int kTmemCols = 512;
 constexpr size_t smem_bytes() { return 1024 + STAGES * STAGE_BYTES + kStaging + 256; }
 static_assert(smem_bytes() <= 232448, "fits the opt-in shared memory of one CTA");
@@ -71,8 +79,9 @@ struct VocabGemmArgs {
   int ldp;               // columns of the stored g (v rounded up to 64)
   const int64_t* targets;
   int64_t ignore;
-  float2* stats;         // M x n_tiles: (maximum, sum of exp(l - maximum))
-  float* target_logit;   // M
+  float2* stats;         // M x pieces: (reference point, sum of exp(l - reference))
+  float* target_logit;   // M: the targets' logits, from this product
+  const float* ref;      // kVocabScaled: the same, known beforehand: the reference points
   const float* lse;      // kVocabProb
   const float* dloss;
   const float* dlse;     // or NULL
@@ -82,12 +91,6 @@ struct VocabGemmArgs {
   const float* target_factor;
   const uint16_t* W;
 };
-
-__device__ __forceinline__ uint32_t tmem_ld_1(uint32_t taddr) {
-  uint32_t v;
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(v) : "r"(taddr));
-  return v;
-}
 
 struct VocabItem {
   int m0, n0, nt, kb0, kb1, part;   // part: the partial tile's index, or -1
@@ -163,6 +166,9 @@ __global__ void __launch_bounds__(vg::kThreads, 1)
                       const __grid_constant__ CUtensorMap tmOut, const __grid_constant__ CUtensorMap tmPart,
                       const VocabGemmArgs args) {
   using namespace vg;
+  auto chunk_end = [](const VocabItem& it, int kc) {
+    return kMode == kVocabGrad ? it.kb1 : min(it.kb1, kc + (kc == it.kb0 ? 2 * CHUNK : CHUNK));
+  };
   constexpr bool kBmn = kMode == kVocabGrad;   // W as the K-major operand (logits) or the MN-major one
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -255,30 +261,33 @@ __global__ void __launch_bounds__(vg::kThreads, 1)
       const uint32_t b_lo0 = sw128_desc_lo(smem_addr(smem) + A_BYTES, kBmn ? 8192 : 16);
       int g = 0, n = 0;
       bool ok = true;
-      for (int item = pair; ok && item < args.items; item += pairs, ++n) {
+      for (int item = pair; ok && item < args.items; item += pairs) {
         const VocabItem it = vocab_item(args, item);
-        const int buf = n & 1;
-        if (!mbar_wait_warp(&acc_empty[buf], ((n >> 1) & 1) ^ 1u, abort_flag)) break;
-        tc_fence_after();
-        for (int kb = it.kb0; kb < it.kb1; ++kb, ++g) {
-          const int slot = g % STAGES;
-          const uint32_t ph = (g / STAGES) & 1;
-          if (!mbar_wait_warp(&full[slot], ph, abort_flag)) { ok = false; break; }
+        for (int kc = it.kb0, ke; ok && kc < it.kb1; kc = ke, ++n) {   // one accumulation
+          const int buf = n & 1;
+          ke = chunk_end(it, kc);
+          if (!mbar_wait_warp(&acc_empty[buf], ((n >> 1) & 1) ^ 1u, abort_flag)) { ok = false; break; }
           tc_fence_after();
-          const uint32_t a_lo = a_lo0 + slot * (STAGE_BYTES >> 4), b_lo = b_lo0 + slot * (STAGE_BYTES >> 4);
-          if (elect_one()) {
+          for (int kb = kc; kb < ke; ++kb, ++g) {
+            const int slot = g % STAGES;
+            const uint32_t ph = (g / STAGES) & 1;
+            if (!mbar_wait_warp(&full[slot], ph, abort_flag)) { ok = false; break; }
+            tc_fence_after();
+            const uint32_t a_lo = a_lo0 + slot * (STAGE_BYTES >> 4), b_lo = b_lo0 + slot * (STAGE_BYTES >> 4);
+            if (elect_one()) {
 #pragma unroll
-            for (int k = 0; k < KS * (BK / 16); ++k) {
-              const uint32_t s = (k / (BK / 16)) * (ATOM >> 4), kk = k % (BK / 16);
-              umma2_bf16(tmem_base + buf * BN, sw128_desc_of(a_lo + s + kk * 2),
-                         sw128_desc_of(b_lo + s + kk * (kBmn ? 128 : 2)), kIdesc, (kb > it.kb0 || k > 0) ? 1u : 0u);
+              for (int k = 0; k < KS * (BK / 16); ++k) {
+                const uint32_t s = (k / (BK / 16)) * (ATOM >> 4), kk = k % (BK / 16);
+                umma2_bf16(tmem_base + buf * BN, sw128_desc_of(a_lo + s + kk * 2),
+                           sw128_desc_of(b_lo + s + kk * (kBmn ? 128 : 2)), kIdesc, (kb > kc || k > 0) ? 1u : 0u);
+              }
+              umma2_commit_multicast(&empty[slot], 0x3);   // frees the stage in both CTAs
             }
-            umma2_commit_multicast(&empty[slot], 0x3);   // frees the stage in both CTAs
+            __syncwarp();
           }
+          if (elect_one()) umma2_commit_multicast(&acc_full[buf], 0x3);
           __syncwarp();
         }
-        if (elect_one()) umma2_commit_multicast(&acc_full[buf], 0x3);
-        __syncwarp();
       }
       // every MMA has read its operands before the CTAs leave (elect picks the lane that issued them)
       if (elect_one()) {
@@ -288,162 +297,163 @@ __global__ void __launch_bounds__(vg::kThreads, 1)
       __syncwarp();
     }
   } else {
-    // ---------------- epilogue: warp w has accumulator rows 32 w .. of this CTA, a row per lane ----
-    uint8_t* stage = staging + warp * 8192;
-    int n = 0, round = 0;
-    // a 32-row x 128-byte tile, 128-byte swizzled as the output maps expect, alternating two
-    auto begin_tile = [&]() {
-      if (lane == 0) bulk_wait_group_read<1>();   // the store issued two rounds ago has read its tile
+    // -------- epilogue: warp w has accumulator rows 32 (w mod 4) .. of this CTA, a row per lane, and the
+    // columns 128 (w / 4) .. of the tile --------
+    uint8_t* stage = staging + warp * 4096;
+    const int quad = warp & 3, half = warp >> 2;
+    int n = 0;
+    // Stores 32 rows x 128 bytes at (x, y) of `map`: each lane's row as eight 16-byte chunks, 128-byte
+    // swizzled (eight lanes' stores hit eight bank groups), by one TMA store.
+    auto store_tile = [&](const uint4 (&q)[8], const CUtensorMap* map, int x, int y, bool any) {
+      if (lane == 0) bulk_wait_group_read<0>();   // the store before has read the tile
       __syncwarp();
-      return stage + (round++ & 1) * 4096;
-    };
-    auto end_tile = [&](const uint8_t* buf, const CUtensorMap* map, int x, int y, bool any) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) *reinterpret_cast<uint4*>(stage + lane * 128 + ((k ^ (lane & 7)) << 4)) = q[k];
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
-        if (any) tma_store_2d(map, buf, x, y);
+        if (any) tma_store_2d(map, stage, x, y);
         bulk_commit_group();
       }
     };
-    for (int item = pair; item < args.items; item += pairs, ++n) {
-      const VocabItem it = vocab_item(args, item);
-      const int buf = n & 1;
-      // One lane polls, with pauses: 128 threads polling the barrier through a whole main loop take
-      // the shared-memory bandwidth that the MMAs read their operands with.
+    // One lane polls, with pauses: 256 threads polling the barrier through a whole main loop take
+    // shared-memory bandwidth that the MMAs read their operands with.
+    auto wait_acc = [&]() {
       bool ready = true;
       if (lane == 0) {
-        for (int i = 0; i < 4096 && !mbar_try_wait(&acc_full[buf], (n >> 1) & 1) && !*abort_flag; ++i) __nanosleep(100);
-        ready = mbar_wait(&acc_full[buf], (n >> 1) & 1, abort_flag);
+        for (int i = 0; i < 16384 && !mbar_try_wait(&acc_full[n & 1], (n >> 1) & 1) && !*abort_flag; ++i) __nanosleep(32);
+        ready = mbar_wait(&acc_full[n & 1], (n >> 1) & 1, abort_flag);
       }
-      if (!__shfl_sync(0xFFFFFFFFu, ready, 0)) break;
+      ready = __shfl_sync(0xFFFFFFFFu, ready, 0);
       tc_fence_after();
-      const uint32_t taddr = tmem_base + (static_cast<uint32_t>(warp * 32) << 16) + static_cast<uint32_t>(buf * BN);
-      const int row0 = it.m0 + rank * 128 + warp * 32, row = row0 + lane;
-      const bool rok = row < args.M;
-      auto load64 = [&](int c, uint32_t (&v)[64]) {   // columns c .. c + 63 of this lane's row
+      return ready;
+    };
+    const uint32_t lane_addr = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(half * PIECE);
+    auto load64 = [&](int c, uint32_t (&v)[64]) {   // columns c .. c + 63 of this lane's row
 #pragma unroll
-        for (int q = 0; q < 4; ++q) tmem_ld_16(taddr + c + 16 * q, *reinterpret_cast<uint32_t(*)[16]>(&v[16 * q]));
-        tmem_ld_wait();
-      };
-      auto drained_acc = [&]() {   // the last TMEM read of this tile is behind
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_pair(&acc_empty[buf], 0);
-      };
+      for (int q = 0; q < 4; ++q)
+        tmem_ld_16(lane_addr + (n & 1) * BN + c + 16 * q, *reinterpret_cast<uint32_t(*)[16]>(&v[16 * q]));
+      tmem_ld_wait();
+    };
+    auto release_acc = [&]() {   // the last read of this accumulation is behind
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_pair(&acc_empty[n & 1], 0);
+      ++n;
+    };
+    bool ok = true;
+    for (int item = pair; ok && item < args.items; item += pairs) {
+      const VocabItem it = vocab_item(args, item);
+      const int row0 = it.m0 + rank * 128 + quad * 32, row = row0 + lane;
+      const int n0 = it.n0 + half * PIECE;   // this warp's first column
+      const bool rok = row < args.M;
       if (kMode == kVocabGrad) {
-        if (it.part < 0) {
-          const RowFactor rf = row_factor(args, rok ? row : -1);
-          for (int c = 0; c < BN; c += 64) {
-            uint32_t v[64];
-            load64(c, v);
-            if (c + 64 == BN) drained_acc();
-            if (it.n0 + c >= args.N) continue;
-            uint8_t* tile = begin_tile();
-            uint8_t* rowp = tile + lane * 128;
+        if (!wait_acc()) break;
+        const RowFactor rf = row_factor(args, it.part < 0 && rok ? row : -1);
+#pragma unroll 1
+        for (int c = 0; c < PIECE; c += 64) {
+          uint32_t v[64];
+          load64(c, v);
+          if (c + 64 == PIECE) release_acc();
+          uint4 q[8];
+          if (it.part < 0) {
+            if (n0 + c >= args.N) continue;
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
               float f[8];
 #pragma unroll
               for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(v[8 * k + e]);
-              if (it.n0 + c + 8 * k < args.N) rf.apply(f, it.n0 + c + 8 * k);
-              *reinterpret_cast<uint4*>(rowp + ((k ^ (lane & 7)) << 4)) = pack8(f);
+              if (n0 + c + 8 * k < args.N) rf.apply(f, n0 + c + 8 * k);
+              q[k] = pack8(f);
             }
-            end_tile(tile, &tmOut, it.n0 + c, row0, row0 < args.M);
-          }
-        } else {
-          for (int c = 0; c < BN; c += 64) {
-            uint32_t v[64];
-            load64(c, v);
-            if (c + 64 == BN) drained_acc();
+            store_tile(q, &tmOut, n0 + c, row0, row0 < args.M);
+          } else {
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              uint8_t* tile = begin_tile();
-              uint8_t* rowp = tile + lane * 128;
+            for (int part = 0; part < 2; ++part) {
 #pragma unroll
               for (int k = 0; k < 8; ++k)
-                *reinterpret_cast<uint4*>(rowp + ((k ^ (lane & 7)) << 4)) =
-                    make_uint4(v[32 * half + 4 * k], v[32 * half + 4 * k + 1], v[32 * half + 4 * k + 2],
-                               v[32 * half + 4 * k + 3]);
-              end_tile(tile, &tmPart, c + 32 * half, it.part * BM + rank * 128 + warp * 32, true);
+                q[k] = make_uint4(v[32 * part + 4 * k], v[32 * part + 4 * k + 1], v[32 * part + 4 * k + 2],
+                                  v[32 * part + 4 * k + 3]);
+              store_tile(q, &tmPart, half * PIECE + c + 32 * part, it.part * BM + rank * 128 + quad * 32, true);
             }
           }
         }
         continue;
       }
-      // ---- logits: columns behind the vocabulary read as zero products and count as -inf ----------
-      const int vcols = min(BN, args.N - it.n0);   // > 0
+      // ---- logits ----------------------------------------------------------------------------------
+      float s[PIECE];
+#pragma unroll
+      for (int e = 0; e < PIECE; ++e) s[e] = 0.f;
+#pragma unroll 1
+      for (int kc = it.kb0; kc < it.kb1; kc = chunk_end(it, kc)) {
+        if (!wait_acc()) { ok = false; break; }
+#pragma unroll
+        for (int c = 0; c < PIECE; c += 16) {   // (16 at a time: the sums leave no room for more)
+          uint32_t v[16];
+          tmem_ld_16(lane_addr + (n & 1) * BN + c, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 16; ++e) s[c + e] += __uint_as_float(v[e]);
+        }
+        release_acc();
+      }
+      if (!ok) break;
+      const int vcols = args.N - n0;   // columns behind the vocabulary read as zero products and count as -inf
+      if (vcols < PIECE) {
+#pragma unroll
+        for (int e = 0; e < PIECE; ++e) s[e] = e < vcols ? s[e] : -INFINITY;
+      }
       const int64_t y = rok ? __ldg(args.targets + row) : -1;
       const bool counted = y >= 0 && y < args.N && y != args.ignore;
-      const int tcol = counted && y >= it.n0 && y < it.n0 + BN ? static_cast<int>(y - it.n0) : -1;
-      if (kMode == kVocabStats || kMode == kVocabScaled) {
-        constexpr bool kScaled = kMode == kVocabScaled;
-        // the target's logit, for the few rows whose target lies in this piece (kVocabScaled has it)
-        for (unsigned left = kScaled ? 0u : __ballot_sync(0xFFFFFFFFu, tcol >= 0); left; left &= left - 1) {
-          const int src = __ffs(left) - 1;
-          const uint32_t v = tmem_ld_1(taddr + __shfl_sync(0xFFFFFFFFu, tcol, src));
-          tmem_ld_wait();
-          if (lane == src) args.target_logit[row] = __uint_as_float(v);
-        }
-        float m = -INFINITY;
-        for (int c = 0; c < vcols; c += 64) {
-          uint32_t v[64];
-          load64(c, v);
-#pragma unroll
-          for (int e = 0; e < 64; ++e) m = fmaxf(m, c + e < vcols ? __uint_as_float(v[e]) : -INFINITY);
-        }
-        const RowRef rr = row_ref<kScaled>(m, kScaled && counted ? __ldg(args.target_logit + row) : 0.f, counted);
-        if (kScaled && rr.redo) *args.redo = 1u;
-        float s0 = 0.f, s1 = 0.f;
-        for (int c = 0; c < BN; c += 64) {
-          if (c >= vcols && (!kScaled || it.n0 + c >= args.ldp)) break;
-          uint32_t v[64];
-          load64(c, v);
-          float p[64];
-#pragma unroll
-          for (int e = 0; e < 64; ++e) p[e] = c + e < vcols ? ex2(fmaf(__uint_as_float(v[e]), kLog2e, -rr.base)) : 0.f;
-#pragma unroll
-          for (int e = 0; e < 64; e += 2) {
-            s0 += p[e];
-            s1 += p[e + 1];
-          }
-          if (kScaled) {
-#pragma unroll
-            for (int e = 0; e < 64; ++e) p[e] = c + e == tcol ? 0.f : p[e];
-            uint8_t* tile = begin_tile();
-            uint8_t* rowp = tile + lane * 128;
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              *reinterpret_cast<uint4*>(rowp + ((k ^ (lane & 7)) << 4)) =
-                  pack8(*reinterpret_cast<const float(*)[8]>(&p[8 * k]));
-            end_tile(tile, &tmOut, it.n0 + c, row0, row0 < args.M);
-          }
-        }
-        drained_acc();
-        if (rok) args.stats[static_cast<int64_t>(row) * args.n_tiles + it.nt] = make_float2(rr.ref, s0 + s1);
-      } else {
+      const int tcol = counted && y >= n0 && y < n0 + PIECE ? static_cast<int>(y - n0) : -1;
+      const bool any_target = __any_sync(0xFFFFFFFFu, tcol >= 0);   // few pieces hold a target of the warp's rows
+      if (kMode == kVocabProb) {
         const float b = counted ? __ldg(args.dloss + row) : 0.f;
         const float a = b + (rok && args.dlse ? __ldg(args.dlse + row) : 0.f);
         const float nl = rok ? -__ldg(args.lse + row) * kLog2e : 0.f;
-        for (int c = 0; c < BN && it.n0 + c < args.ldp; c += 64) {
-          uint32_t v[64];
-          load64(c, v);
-          uint8_t* tile = begin_tile();
-          uint8_t* rowp = tile + lane * 128;
+        // a row that counts for nothing is zero whatever its logits are
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            float f[8];
+        for (int e = 0; e < PIECE; ++e) s[e] = a != 0.f ? a * ex2(fmaf(s[e], kLog2e, nl)) : 0.f;
+        if (any_target) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const int col = c + 8 * k + e;
-              // a row that counts for nothing is zero whatever its logits are
-              f[e] = col < vcols && a != 0.f ? a * ex2(fmaf(__uint_as_float(v[8 * k + e]), kLog2e, nl)) : 0.f;
-              if (col == tcol) f[e] -= b;
-            }
-            *reinterpret_cast<uint4*>(rowp + ((k ^ (lane & 7)) << 4)) = pack8(f);
-          }
-          end_tile(tile, &tmOut, it.n0 + c, row0, row0 < args.M);
+          for (int e = 0; e < PIECE; ++e) s[e] -= e == tcol ? b : 0.f;
         }
-        drained_acc();
+      } else {
+        constexpr bool kScaled = kMode == kVocabScaled;
+        if (any_target) {
+          float ty = 0.f;
+#pragma unroll
+          for (int e = 0; e < PIECE; ++e) ty = e == tcol ? s[e] : ty;
+          if (tcol >= 0) args.target_logit[row] = ty;
+        }
+        float m = s[0];
+#pragma unroll
+        for (int e = 1; e < PIECE; ++e) m = fmaxf(m, s[e]);
+        const RowRef rr = row_ref<kScaled>(m, kScaled && counted ? __ldg(args.ref + row) : 0.f, counted);
+        if (kScaled && rr.redo) *args.redo = 1u;
+        float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+        for (int e = 0; e < PIECE; e += 2) {
+          s[e] = ex2(fmaf(s[e], kLog2e, -rr.base));
+          s[e + 1] = ex2(fmaf(s[e + 1], kLog2e, -rr.base));
+          s0 += s[e];
+          s1 += s[e + 1];
+        }
+        if (rok) args.stats[(static_cast<int64_t>(row) * args.n_tiles + it.nt) * (BN / PIECE) + half] = make_float2(rr.ref, s0 + s1);
+        if (kScaled && any_target) {
+#pragma unroll
+          for (int e = 0; e < PIECE; ++e) s[e] = e == tcol ? 0.f : s[e];
+        }
+      }
+      if (kMode != kVocabStats) {
+#pragma unroll
+        for (int c = 0; c < PIECE; c += 64) {
+          if (n0 + c >= args.ldp) break;
+          uint4 q[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) q[k] = pack8(*reinterpret_cast<const float(*)[8]>(&s[c + 8 * k]));
+          store_tile(q, &tmOut, n0 + c, row0, row0 < args.M);
+        }
       }
     }
     if (lane == 0) bulk_wait_group<0>();   // the output is written before the CTA retires
@@ -467,7 +477,9 @@ __global__ void __launch_bounds__(vg::kThreads, 1)
 // column is one reduction instruction, the sums of 16 columns 16 shuffles.
 // ------------------------------------------------------------------------------------------
 namespace vn {
-constexpr int kMaxTokens = 256;   // one MMA's columns
+constexpr int kMaxTokens = 80;    // an epilogue thread's sums: one register per token
+// stages of the accumulation that starts at stage kc: K = 512 (1024 for a tile's first), as above
+__host__ __device__ constexpr int chunk(int kc) { return kc == 0 ? 8 : 4; }
 constexpr int BM = 128, BK = 64;
 constexpr int KS = 2;             // K-steps of 64 per stage: a stage's waits and copies cost some 700 cycles
                                   // whatever it holds, so that 16 KB of W each were not enough to keep up with HBM
@@ -499,6 +511,7 @@ struct VocabNarrowArgs {
   int64_t ignore;
   float2* stats;         // t x units
   float* target_logit;
+  const float* ref;
   const float* lse;
   const float* dloss;
   const float* dlse;
@@ -641,7 +654,7 @@ __global__ void __launch_bounds__(vn::kThreads, 1)
     const int64_t y = n < args.t ? args.targets[n] : -1;
     const bool counted = y >= 0 && y < args.v && y != args.ignore;
     t_word[n] = counted ? static_cast<int>(y) : -1;
-    if (kMode == kVocabScaled) t_ref[n] = counted ? args.target_logit[n] : 0.f;
+    if (kMode == kVocabScaled) t_ref[n] = counted ? args.ref[n] : 0.f;
     if (kMode == kVocabProb) {
       const float b = counted ? args.dloss[n] : 0.f;
       t_b[n] = b;
@@ -683,31 +696,54 @@ __global__ void __launch_bounds__(vn::kThreads, 1)
     int n = 0;
     // (a last tile of fewer than four units leaves the other rows of its operand as they were: their
     // accumulator rows are not read)
-    for (int u = u0; u < u1; u += 4, ++n)
-      if (!narrow_mma<false>(cta, args.n16, n & 1, n, args.num_kb, g)) break;
+    bool ok = true;
+    for (int u = u0; ok && u < u1; u += 4)
+      for (int kc = 0; ok && kc < args.num_kb; kc += chunk(kc), ++n)
+        ok = narrow_mma<false>(cta, args.n16, n & 1, n, min(chunk(kc), args.num_kb - kc), g);
     narrow_drain_mma(cta, g);
   } else {
     int n = 0;
-    for (int u = u0; u < u1; u += 4, ++n) {
-      const int buf = n & 1;
-      if (!mbar_wait_warp(&cta.acc_full[buf], (n >> 1) & 1, cta.abort_flag)) break;
-      tc_fence_after();
-      const int unit = u + warp;
-      if (unit < u1) {
+    bool ok = true;
+    for (int u = u0; ok && u < u1; u += 4) {
+      float s[kMaxTokens];
+#pragma unroll
+      for (int j = 0; j < kMaxTokens; ++j) s[j] = 0.f;
+#pragma unroll 1
+      for (int kc = 0; kc < args.num_kb; kc += chunk(kc), ++n) {
+        const int buf = n & 1;
+        if (!mbar_wait_warp(&cta.acc_full[buf], (n >> 1) & 1, cta.abort_flag)) { ok = false; break; }
+        tc_fence_after();
         const uint32_t taddr = cta.tmem + (static_cast<uint32_t>(warp * 32) << 16) + buf * (cta.tmem_cols / 2);
+        if (u + warp < u1) {
+#pragma unroll
+          for (int c = 0; c < kMaxTokens; c += 16) {
+            if (c >= args.n16) break;
+            uint32_t v[16];
+            tmem_ld_16(taddr + c, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) s[c + j] += __uint_as_float(v[j]);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&cta.acc_empty[buf]);
+      }
+      const int unit = u + warp;
+      if (ok && unit < u1) {
         const int word = unit * kUnit + lane;
         const bool wok = word < args.v;
-        for (int c = 0; c < args.n16; c += 16) {
-          uint32_t v[16];
-          tmem_ld_16(taddr + c, v);
-          tmem_ld_wait();
+#pragma unroll
+        for (int c = 0; c < kMaxTokens; c += 16) {
+          if (c >= args.n16) break;
+          const float* v = &s[c];
           float p[16];
           if (kMode == kVocabProb) {
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
               const float a = t_a[c + j];
               // a row that counts for nothing is zero whatever its logits are
-              p[j] = wok && a != 0.f ? a * ex2(fmaf(__uint_as_float(v[j]), vg::kLog2e, t_ref[c + j])) : 0.f;
+              p[j] = wok && a != 0.f ? a * ex2(fmaf(v[j], vg::kLog2e, t_ref[c + j])) : 0.f;
               if (word == t_word[c + j]) p[j] -= t_b[c + j];
             }
           } else {
@@ -715,11 +751,11 @@ __global__ void __launch_bounds__(vn::kThreads, 1)
             float mine = 0.f;    // the reference of this lane's token (lane / 2) below
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
-              const float l = wok ? __uint_as_float(v[j]) : -INFINITY;
+              const float l = wok ? v[j] : -INFINITY;
               const int w = t_word[c + j];
               const RowRef rr = row_ref<kScaled>(warp_max(l), kScaled ? t_ref[c + j] : 0.f, w >= 0);
               if (kScaled && rr.redo && lane == 0) *args.redo = 1u;
-              if (!kScaled && word == w) args.target_logit[c + j] = l;
+              if (word == w) args.target_logit[c + j] = l;
               if ((lane >> 1) == j) mine = rr.ref;
               p[j] = wok ? ex2(fmaf(l, vg::kLog2e, -rr.base)) : 0.f;
             }
@@ -752,9 +788,6 @@ __global__ void __launch_bounds__(vn::kThreads, 1)
           }
         }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&cta.acc_empty[buf]);
     }
   }
   narrow_end(cta);
@@ -834,6 +867,7 @@ __global__ void __launch_bounds__(vn::kThreads, 1)
 struct VocabRowArgs {
   const float2* stats;        // t x pieces
   const float* target_logit;
+  const float* ref;           // with dloss: what the stored exponentials are relative to
   const int64_t* targets;
   int64_t ignore;
   int t, v, pieces;
@@ -890,7 +924,7 @@ __global__ void __launch_bounds__(256) vocab_rows_kernel(const VocabRowArgs a) {
   a.lse[row] = lse;
   if (a.dloss) {
     const float d = counted ? a.dloss[row] : 0.f;
-    a.factor[row] = counted ? d * expf(-loss) : 0.f;          // dloss . p[y]
+    a.factor[row] = counted ? d * expf(a.ref[row] - lse) : 0.f;
     a.target_factor[row] = counted ? d * expm1f(-loss) : 0.f;  // dloss . (p[y] - 1)
   }
 }
@@ -899,7 +933,7 @@ __global__ void __launch_bounds__(256) vocab_rows_kernel(const VocabRowArgs a) {
 template <int kWarps>
 __global__ void __launch_bounds__(256)
     vocab_target_kernel(const uint16_t* X, const uint16_t* W, const int64_t* targets, int64_t ignore, int t, int h,
-                        int v, float* target_logit, unsigned* redo) {
+                        int v, float* ref, unsigned* redo) {
   __shared__ float sh[8];
   const int row = blockIdx.x * (8 / kWarps) + (threadIdx.x >> 5) / kWarps, lane = threadIdx.x & 31;
   if (blockIdx.x == 0 && threadIdx.x == 0) *redo = 0u;
@@ -924,7 +958,7 @@ __global__ void __launch_bounds__(256)
     if (threadIdx.x == 0)
       for (int w = 1; w < kWarps; ++w) s += sh[w];
   }
-  if (threadIdx.x % (32 * kWarps) == 0) target_logit[row] = s;
+  if (threadIdx.x % (32 * kWarps) == 0) ref[row] = s;
 }
 
 // dX tiles whose K was split: the partial tiles are added in order and rounded once.

@@ -95,6 +95,23 @@ def test_forward_backward_and_both_at_once(t, h, v):
     assert B.last_status() == 0
 
 
+@pytest.mark.parametrize("t", [20, 300])
+@pytest.mark.parametrize("lean", [0.0, 1.0])
+def test_logits_are_summed_in_pieces(t, lean):
+    """One word, so that lse is its logit, over 8192 inputs that all add up (lean 1) or cancel. The
+    tensor core truncates its sum every 16 inputs, and the kernels sum at most 1024 inputs there: 64
+    truncations of 2^-23 of the magnitudes at most, 16 more for the products of one step, and a few
+    for adding the pieces. Summed in one piece it would be 512 truncations (measured 2.7e-5)."""
+    h = 8192
+    W = randn((1, h), 1.0, 3).cuda()
+    X = ((1 - lean) * randn((t, h), 1.0, 4).float().cuda() + lean * W.float()).bfloat16()
+    y = torch.zeros(t, dtype=torch.int64, device="cuda")
+    loss, lse = B.qlora_vocab_loss_fwd(X, W, y)
+    want = (X.double() @ W.double().T)[:, 0]
+    assert_within(lse, want, (64 + 16 + 10) * 2 * U32 * (X.double().abs() @ W.double().abs().T)[:, 0], "lse")
+    assert not loss.any()
+
+
 def test_reference_gradient_against_differences():
     t, h, v = 5, 16, 40
     X, W, y = randn((t, h), 1.0, 1).double(), randn((v, h), 0.7, 2).double(), torch.tensor([3, -100, 39, 0, 3])
