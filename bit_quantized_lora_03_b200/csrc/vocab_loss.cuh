@@ -156,7 +156,7 @@ __device__ __forceinline__ RowRef row_ref(float m, float c, bool counted) {
   RowRef r;
   r.redo = kScaled && counted && m - c > 60.f;
   r.ref = kScaled && counted && !r.redo ? c : m;
-  r.base = (fabsf(r.ref) == INFINITY ? 0.f : r.ref) * vg::kLog2e;
+  r.base = fabsf(r.ref) == INFINITY ? 0.f : r.ref;
   return r;
 }
 
@@ -434,8 +434,8 @@ __global__ void __launch_bounds__(vg::kThreads, 1)
         float s0 = 0.f, s1 = 0.f;
 #pragma unroll
         for (int e = 0; e < PIECE; e += 2) {
-          s[e] = ex2(fmaf(s[e], kLog2e, -rr.base));
-          s[e + 1] = ex2(fmaf(s[e + 1], kLog2e, -rr.base));
+          s[e] = ex2((s[e] - rr.base) * kLog2e);   // (exact near the reference, which a product with
+          s[e + 1] = ex2((s[e + 1] - rr.base) * kLog2e);   // log2 e rounded first would not be)
           s0 += s[e];
           s1 += s[e + 1];
         }
@@ -757,7 +757,7 @@ __global__ void __launch_bounds__(vn::kThreads, 1)
               if (kScaled && rr.redo && lane == 0) *args.redo = 1u;
               if (word == w) args.target_logit[c + j] = l;
               if ((lane >> 1) == j) mine = rr.ref;
-              p[j] = wok ? ex2(fmaf(l, vg::kLog2e, -rr.base)) : 0.f;
+              p[j] = wok ? ex2((l - rr.base) * vg::kLog2e) : 0.f;
             }
             float q[16];
 #pragma unroll
