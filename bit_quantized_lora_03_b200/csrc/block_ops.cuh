@@ -67,12 +67,12 @@ NormBwdPlan plan_norm_bwd(int64_t t, int64_t h, int sms) {
   return p;
 }
 
-
 // ------------------------------------------------------------------------------------------
 // vocabulary loss
 // ------------------------------------------------------------------------------------------
-// Tokens whose g (or scaled exponentials) the workspace holds at a time: as many as fit 256 MiB,
-// at least one row of tiles. Few long runs keep the second product's tiles busy and read W seldom.
+// Tokens whose g (or scaled exponentials; for the loss alone, statistics) the workspace holds at a time: as
+// many as fit 256 MiB, at least one row of tiles. Few long runs keep the second product's tiles busy and
+// read W seldom.
 constexpr size_t kVocabRunBytes = size_t(256) << 20;
 constexpr int64_t kVocabMaxV = int64_t(1) << 24;
 constexpr int kVocabMaxParts = kMaxSms;   // partial tiles of a split K
@@ -95,8 +95,8 @@ VocabPlan plan_vocab(int64_t t, int64_t h, int64_t v, bool stats, bool grad) {
   p.narrow = t <= kVocabNarrowTokens;
   p.ldp = (v + 63) / 64 * 64;
   p.pieces = p.narrow ? p.ldp / vn::kUnit : (v + vg::BN - 1) / vg::BN * (vg::BN / vg::PIECE);
-  const int64_t fit = static_cast<int64_t>(kVocabRunBytes / (static_cast<size_t>(p.ldp) * 2));
-  p.run = grad ? std::min<int64_t>(t, std::max<int64_t>(vg::BM, fit / vg::BM * vg::BM)) : t;
+  const int64_t fit = static_cast<int64_t>(kVocabRunBytes) / (grad ? p.ldp * 2 : p.pieces * 8);
+  p.run = std::min<int64_t>(t, std::max<int64_t>(vg::BM, fit / vg::BM * vg::BM));
   if (grad) {
     p.g_bytes = align256(static_cast<size_t>(p.run) * p.ldp * 2);
     p.part_bytes = p.narrow ? static_cast<size_t>(kMaxSms + (h + vn::BM - 1) / vn::BM) * vn::BM *

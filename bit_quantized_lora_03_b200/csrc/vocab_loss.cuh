@@ -33,9 +33,11 @@
 //
 // Bound: the tensor cores (2thv per product) for more than a few hundred tokens, reading W for few.
 // The design follows from the first: cta_group::2 (256 x 256 x 16 per instruction, each CTA loading
-// half of A and half of B), a six-stage TMA ring, and two accumulators in tensor memory, so that a
-// tile's epilogue (eight warps) runs under the next tile's products. g is rounded to bf16 because it
-// is an operand of a bf16 product: a relative 2^-9 per term, against the 2^-9 of dX's own rounding.
+// half of A and half of B), a TMA ring of three stages of two K-steps, and two accumulators in tensor
+// memory, so that a tile's epilogue (eight warps) runs under the next tile's products. g is rounded to
+// bf16 because it is an operand of a bf16 product: 2^-8 of each term at most, as dX's own rounding.
+// Measured on 32000 x 4096, 4096 tokens: loss and gradient 1610 us, two products at 1.33 PFLOP/s, where
+// the card is at its power limit (1.39 in a plain bf16 product); 1 token: loss 54 us, W read once.
 //
 // Every wait is bounded (qlora::mbar_wait); on expiry the CTA reports QLORA_DEV_TIMEOUT, stops
 // issuing, waits for its own copies and MMAs in flight, frees TMEM and returns.
@@ -532,7 +534,7 @@ struct NarrowCta {
   uint64_t *full, *empty, *acc_full, *acc_empty;
   uint32_t* tmem_holder;
   volatile uint32_t* abort_flag;
-  float* token;          // 5 x 256 values per token
+  float* token;          // 5 values per token
   int stages, stage_bytes;
   uint32_t tmem_cols, tmem;
 };

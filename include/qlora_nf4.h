@@ -436,8 +436,9 @@ QLORA_API size_t qlora_norm_residual_bwd_workspace_bytes(int64_t t, int64_t h);
  * frozen like every base weight here and gets no gradient. With logits l = X.W^T, in fp32:
  *   lse_i  = log sum_v exp(l_iv),   loss_i = lse_i - l_i[y_i],
  *   dX_i   = sum_v (a_i exp(l_iv - lse_i) - b_i [v = y_i]) W_v,  b_i = dloss_i, a_i = b_i + dlse_i.
- * The vocabulary is walked in pieces; the t x v logits are never stored. The calls with a gradient
- * hold the bf16 factors of W_v for a bounded run of tokens (256 MiB) in the workspace at a time.
+ * The vocabulary is walked in pieces; the t x v logits are never stored. The workspace holds the
+ * statistics of those pieces, and for a gradient the bf16 factors of W_v, for a run of tokens at a
+ * time: as many as fit 256 MiB, or 256 tokens where those need more (v above 2^19).
  *   X        device bf16, t x h row-major.  8 <= h, h % 8 == 0.
  *   W        device bf16, v x h row-major (one row per word of the vocabulary). 1 <= v <= 2^24.
  *   targets  device int64, t, 8-byte aligned. A target equal to ignore_index is not counted: its

@@ -106,6 +106,16 @@ def test_vocabulary_loss(lib):
     assert lib.qlora_vocab_loss_bwd_workspace_bytes(1 << 20, 4096, 32000) <= bound
 
 
+def test_vocabulary_loss_workspace_is_bounded(lib):
+    """The loss alone holds 8 bytes per token and 128 words (or 32, for few tokens) of one run."""
+    size = lib.qlora_vocab_loss_fwd_workspace_bytes
+    assert size(1 << 20, 4096, 1 << 17) <= (256 << 20) + 4 * 4 * (1 << 18) + 4096
+    assert size(1 << 30, 8, 1 << 24) <= (256 << 20) + 4 * 4 * 256 + 4096
+    assert size(4096, 4096, 32000) >= 4096 * 250 * 8
+    # 256 tokens where those need more than 256 MiB
+    assert lib.qlora_vocab_loss_bwd_workspace_bytes(1 << 20, 8, 1 << 24) >= 256 * (1 << 24) * 2
+
+
 def test_binding_refuses_host_tensors_shapes_and_unknown_activations():
     x = torch.zeros(4, 64, dtype=torch.bfloat16)
     p = B.PackedNF4(64, 64, "cpu")

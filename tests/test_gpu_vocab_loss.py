@@ -95,6 +95,30 @@ def test_forward_backward_and_both_at_once(t, h, v):
     assert B.last_status() == 0
 
 
+@pytest.mark.parametrize("t,v,rows", [(3, 1 << 24, [0, 1, 2]), (260, 1 << 24, [0, 3, 255, 256, 259]),
+                                      (4100, 1 << 20, [0, 4095, 4096, 4099])])
+def test_long_vocabularies(t, v, rows):
+    """The largest vocabulary (g and the statistics pass 2^32 bytes, t x v passes 2^32), and the loss
+    alone in more than one run. Some rows are compared. A row's sum of exponentials goes through 64
+    additions in a piece of 128 and at most 512 + 8 of pieces in a lane, and 13 joins: 600 roundings."""
+    h = 8
+    X, W, y = _inputs(t, h, v, 11)
+    if t > 3:
+        y[3] = 5
+    dloss = torch.full((t,), 1.0 / t, device="cuda")
+    at = torch.tensor(rows, device="cuda")
+    ref = _reference(X[at], W, y[at], dloss[at])
+    ref[2], ref[3] = ref[2] + 600 * U32, ref[3] + 600 * U32
+    ref[5] = ref[5] + 600 * U32 * (dloss[at].double()[:, None] * W.double().abs().amax(0))
+    loss, lse = B.qlora_vocab_loss_fwd(X, W, y)
+    _check_forward(loss[at], lse[at], ref)
+    loss2, lse2, dX = B.qlora_vocab_loss_fwd_bwd(X, W, y, dloss)
+    _check_forward(loss2[at], lse2[at], ref)
+    _check_gradient(dX[at], ref, h, v)
+    _check_gradient(B.qlora_vocab_loss_bwd(X, W, y, lse, dloss)[at], ref, h, v)
+    assert B.last_status() == 0
+
+
 @pytest.mark.parametrize("t", [20, 300])
 @pytest.mark.parametrize("lean", [0.0, 1.0])
 def test_logits_are_summed_in_pieces(t, lean):
