@@ -360,9 +360,12 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
           if (!mbar_wait_warp(&full_p[pslot], (i / P_STAGES) & 1, abort_flag)) { ok = false; break; }
           const uint4* cp = reinterpret_cast<const uint4*>(sP + pslot * P_BYTES + pk_off);
           const uint4 c0 = cp[0], c1 = cp[1];
+          const ProdTab tab = build_prod_tab(lv2, k);
+          // The slot is refilled by the async proxy, which an arrival alone does not hold back behind
+          // loads that are still queued: without the fence a refill overtook them now and then.
+          fence_proxy_async_smem();
           __syncwarp();   // every lane has its codes
           if (lane == 0) mbar_arrive(&empty_p[pslot]);
-          const ProdTab tab = build_prod_tab(lv2, k);
           if (!mbar_wait_warp(&empty[slot], ph ^ 1u, abort_flag)) { ok = false; break; }
           if (valid) {
             const uint32_t words[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
