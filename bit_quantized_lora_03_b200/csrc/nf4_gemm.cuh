@@ -50,17 +50,18 @@ constexpr int A_HALF = 128 * BK * 2;       // 16 KB: this CTA's 128 rows of one 
 constexpr int A_BYTES = 2 * A_HALF;        // 32 KB
 constexpr int B_BYTES = BNH * BK * 2;      // 16 KB
 constexpr int P_BYTES = BNH * BK / 2;      // 4 KB of packed codes
-constexpr int P_STAGES = 8;                // their own ring: codes are read into registers and their slot
-constexpr int P_AHEAD = 4;                 // is free long before the step's MMAs, so they run steps ahead
+constexpr int P_STAGES = 8;                // their own ring, filled by a warp of its own: codes are read into
+                                           // registers and their slot is free long before the step's MMAs
 constexpr int kWorkWarps = 8;              // warps 0-7: dequant producers, then epilogue
 constexpr int kGroupWarps = kWorkWarps / 2;  // producers of one stage: warps 0-3 of the even K-steps,
                                              // 4-7 of the odd ones
 constexpr int kTmaWarp = 8;
 constexpr int kMmaWarp = 9;                // even CTA: MMA issuer
-constexpr int kThreads = 10 * 32;
+constexpr int kCodeWarp = 10;              // TMA of the packed codes
+constexpr int kThreads = 11 * 32;
 constexpr int kTmemCols = 512;
 constexpr int kEpiZTile = kWorkWarps * 8192;   // the staging tiles of Z lie behind those of Y
-static_assert(P_AHEAD <= P_STAGES && P_STAGES % 2 == 0, "a code slot belongs to one producer group");
+static_assert(P_STAGES % 2 == 0, "a code slot belongs to one producer group");
 static_assert(2 * kEpiZTile <= STAGES * (A_BYTES + B_BYTES), "staging tiles in the drained stage buffers");
 
 constexpr size_t nf4_gemm_smem_bytes() {
@@ -176,41 +177,28 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
   const uint32_t tmem_base = *tmem_holder;
 
   if (warp == kTmaWarp) {
-    if (lane == 0) {
-      // What the MMA reads is counted on barriers of the even CTA, whose thread issues it, for both
-      // CTAs: the odd CTA's copies and dequantized tiles arrive there directly.
-      const uint32_t full_a0 = cluster_smem_addr(full_a, 0);
-      int issued = 0, codes = 0;   // K-steps whose operand, and whose code, copies were issued
-      auto load_codes = [&](int kb) {
-        const int slot = kb % P_STAGES;
-        if (!mbar_wait(&empty_p[slot], ((kb / P_STAGES) & 1) ^ 1u, abort_flag)) return false;
-        mbar_arrive_expect_tx(&full_p[slot], P_BYTES);
-        if (!kBwd) {
-          tma_load_2d(sP + slot * P_BYTES, &tmP, &full_p[slot], (kb0 + kb) * (BK / 2), nh0);
-        } else {
-          tma_load_2d(sP + slot * P_BYTES, &tmP, &full_p[slot], nh0 / 2, (kb0 + kb) * BK);
-          tma_load_2d(sP + slot * P_BYTES + 2048, &tmP, &full_p[slot], nh0 / 2 + 32, (kb0 + kb) * BK);
-        }
-        codes = kb + 1;
-        return true;
-      };
-      for (int kb = 0; kb < P_AHEAD && kb < nk; ++kb) load_codes(kb);   // (free slots: no wait)
-      for (int i = 0; i < total; ++i) {
-        const int slot = i % STAGES;
-        const uint32_t ph = (i / STAGES) & 1;
-        if (i + P_AHEAD < nk && !load_codes(i + P_AHEAD)) break;
-        if (!mbar_wait(&empty[slot], ph ^ 1u, abort_flag)) break;
+    // What the MMA reads is counted on barriers of the even CTA, whose warp issues it, for both CTAs: the
+    // odd CTA's copies and dequantized tiles arrive there directly. (Warp-uniform code with an elected
+    // issuer, as below: from a branch of one lane a step's copies took 640 cycles to issue, of the 820 of a
+    // whole step at 256 rows or fewer.)
+    const uint32_t full_a0 = cluster_smem_addr(full_a, 0);
+    int issued = 0;   // K-steps whose copies were issued
+    for (int i = 0; i < total; ++i) {
+      const int slot = i % STAGES;
+      const uint32_t ph = (i / STAGES) & 1;
+      if (!mbar_wait_warp(&empty[slot], ph ^ 1u, abort_flag)) break;
+      uint8_t* a_dst = sA + slot * A_BYTES;
+      uint8_t* b_dst = sB + slot * B_BYTES;
+      const uint32_t bar = full_a0 + static_cast<uint32_t>(slot * sizeof(uint64_t));
+      // sT / sU come from the kernel launched just before this one, which may still be running
+      // (programmatic dependent launch): wait for it before the first LoRA load
+      if (i == nk) pdl_wait();
+      if (elect_one()) {
         if (kEpi == kEpiFused && args.epi.residual && i == (total > 16 ? total - 16 : 0)) {
           for (int a = 0; a < nacc; ++a)       // this CTA's 128 rows of each accumulator, 256 columns
             for (int c = 0; c < BN && n0 + c < args.N; c += 64) tma_prefetch_2d(&tmR, n0 + c, mrow + a * 256);
         }
-        uint8_t* a_dst = sA + slot * A_BYTES;
-        uint8_t* b_dst = sB + slot * B_BYTES;
-        const uint32_t bar = full_a0 + static_cast<uint32_t>(slot * sizeof(uint64_t));
         if (i >= nk) {
-          // sT / sU come from the kernel launched just before this one, which may still be
-          // running (programmatic dependent launch): wait for it before the first LoRA load
-          if (i == nk) pdl_wait();
           const int li = i - nk;
           if (rank == 0) mbar_arrive_expect_tx(&full_a[slot], 2 * (a_bytes + B_BYTES));
           tma_load_2d_pair(a_dst, &tmA2, bar, li * BK, mrow);
@@ -228,21 +216,41 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
           tma_load_2d_pair(a_dst, &tmA, bar, (kb0 + i) * BK, mrow);
           if (nacc == 2) tma_load_2d_pair(a_dst + A_HALF, &tmA, bar, (kb0 + i) * BK, mrow + 256);
         }
-        issued = i + 1;
       }
-      if (*abort_flag) {
-        // make sure no copy is still writing this CTA's shared memory before it exits: the odd
-        // CTA's A copies count on its peer's barriers, so it gives them, at most STAGES of them, a
-        // thousand times a copy's latency (and stays until the cluster's barrier below)
-        for (int j = (issued > STAGES ? issued - STAGES : 0); j < issued; ++j) {
-          if (rank == 0) mbar_drain(&full_a[j % STAGES], (j / STAGES) & 1);
-        }
-        for (int j = (codes > P_STAGES ? codes - P_STAGES : 0); j < codes; ++j)
-          mbar_drain(&full_p[j % P_STAGES], (j / P_STAGES) & 1);
-        if (rank != 0)
-          for (int j = 0; j < 2000; ++j) __nanosleep(1000);
-      }
+      __syncwarp();
+      issued = i + 1;
     }
+    if (lane == 0 && *abort_flag) {
+      // make sure no copy is still writing this CTA's shared memory before it exits: the odd
+      // CTA's A copies count on its peer's barriers, so it gives them, at most STAGES of them, a
+      // thousand times a copy's latency (and stays until the cluster's barrier below)
+      if (rank == 0)
+        for (int j = (issued > STAGES ? issued - STAGES : 0); j < issued; ++j)
+          mbar_drain(&full_a[j % STAGES], (j / STAGES) & 1);
+      else
+        for (int j = 0; j < 2000; ++j) __nanosleep(1000);
+    }
+  } else if (warp == kCodeWarp) {
+    int issued = 0;
+    for (int kb = 0; kb < nk; ++kb) {
+      const int slot = kb % P_STAGES;
+      if (!mbar_wait_warp(&empty_p[slot], ((kb / P_STAGES) & 1) ^ 1u, abort_flag)) break;
+      if (elect_one()) {
+        uint8_t* dst = sP + slot * P_BYTES;
+        mbar_arrive_expect_tx(&full_p[slot], P_BYTES);
+        if (!kBwd) {
+          tma_load_2d(dst, &tmP, &full_p[slot], (kb0 + kb) * (BK / 2), nh0);
+        } else {
+          tma_load_2d(dst, &tmP, &full_p[slot], nh0 / 2, (kb0 + kb) * BK);
+          tma_load_2d(dst + 2048, &tmP, &full_p[slot], nh0 / 2 + 32, (kb0 + kb) * BK);
+        }
+      }
+      __syncwarp();
+      issued = kb + 1;
+    }
+    if (lane == 0 && *abort_flag)
+      for (int j = (issued > P_STAGES ? issued - P_STAGES : 0); j < issued; ++j)
+        mbar_drain(&full_p[j % P_STAGES], (j / P_STAGES) & 1);
   } else if (warp == kMmaWarp) {
     if (rank == 0) {
       // M = 256 per instruction (128 rows from each CTA), N = 256 (128 columns from each)

@@ -151,23 +151,23 @@ __global__ void __launch_bounds__(tcg::kThreads, kMinCtas)
   const uint32_t tmem_base = *tmem_holder;
   if (threadIdx.x == 0) QLORA_STAMP(1);
 
-  if (warp == kTmaWarp) {
-    if (lane == 0) {
-      if (args.pdl == kPdlWaitFirst) pdl_wait();  // every global access follows the loads
-      int issued = 0, slot = 0;
-      uint32_t ph = 0;
-      for (int i = 0; i < nk; ++i) {
-        if (!mbar_wait(&empty[slot], ph ^ 1u, abort_flag)) break;
-        const int kb = kb0 + i;
+  if (warp == kTmaWarp) {   // (warp-uniform, an elected lane issuing: one lane's branch takes hundreds of cycles a step)
+    if (args.pdl == kPdlWaitFirst) pdl_wait();  // every global access follows the loads
+    int issued = 0, slot = 0;
+    uint32_t ph = 0;
+    for (int i = 0; i < nk; ++i) {
+      if (!mbar_wait_warp(&empty[slot], ph ^ 1u, abort_flag)) break;
+      const int kb = kb0 + i;
+      uint8_t* a_dst = smem + slot * SB;
+      uint8_t* b_dst = a_dst + A_BYTES;
+      if (elect_one()) {
         mbar_arrive_expect_tx(&full[slot], A_BYTES + bbytes);
-        uint8_t* a_dst = smem + slot * SB;
         if (!A_MN) {
           tma_load_2d(a_dst, &tmA, &full[slot], kb * BK, m0);
         } else {
           tma_load_2d(a_dst, &tmA, &full[slot], m0, kb * BK);
           tma_load_2d(a_dst + 8192, &tmA, &full[slot], m0 + 64, kb * BK);
         }
-        uint8_t* b_dst = a_dst + A_BYTES;
         if (!B_MN) {
           tma_load_2d(b_dst, &tmB, &full[slot], kb * BK, nb0);
         } else {
@@ -175,16 +175,17 @@ __global__ void __launch_bounds__(tcg::kThreads, kMinCtas)
             tma_load_2d(b_dst + a * 8192, &tmB, &full[slot], nb0 + a * 64, kb * BK);
         }
         if (i == 0) QLORA_STAMP(2);
-        issued = i + 1;
-        if (++slot == STAGES) {
-          slot = 0;
-          ph ^= 1u;
-        }
       }
-      if (*abort_flag) {
-        for (int j = (issued > STAGES ? issued - STAGES : 0); j < issued; ++j)
-          mbar_drain(&full[j % STAGES], (j / STAGES) & 1);
+      __syncwarp();
+      issued = i + 1;
+      if (++slot == STAGES) {
+        slot = 0;
+        ph ^= 1u;
       }
+    }
+    if (lane == 0 && *abort_flag) {
+      for (int j = (issued > STAGES ? issued - STAGES : 0); j < issued; ++j)
+        mbar_drain(&full[j % STAGES], (j / STAGES) & 1);
     }
   } else if (warp == kMmaWarp) {
     const uint32_t idesc = idesc_bf16(BM, BNp, A_MN, B_MN);

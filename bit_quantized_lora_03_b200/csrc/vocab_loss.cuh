@@ -218,20 +218,20 @@ __global__ void __launch_bounds__(vg::kThreads, 1)
   const uint32_t tmem_base = *tmem_holder;
 
   if (warp == kTmaWarp) {
-    if (lane == 0) {
-      // both CTAs' copies count on the even CTA's barrier: the MMA issuer waits for one barrier, and
-      // no thread of the odd CTA has to pass the news on (a relay cost 930 cycles a K-step of 512)
-      const uint32_t full0 = cluster_smem_addr(full, 0);
-      int g = 0;
-      bool ok = true;
-      for (int item = pair; ok && item < args.items; item += pairs) {
-        const VocabItem it = vocab_item(args, item);
-        for (int kb = it.kb0; kb < it.kb1; ++kb, ++g) {
-          const int slot = g % STAGES;
-          if (!mbar_wait(&empty[slot], ((g / STAGES) & 1) ^ 1u, abort_flag)) { ok = false; break; }
-          uint8_t* dst = smem + slot * STAGE_BYTES;
+    // both CTAs' copies count on the even CTA's barrier: the MMA issuer waits for one barrier, and
+    // no thread of the odd CTA has to pass the news on (a relay cost 930 cycles a K-step of 512)
+    const uint32_t full0 = cluster_smem_addr(full, 0);
+    int g = 0;
+    bool ok = true;
+    for (int item = pair; ok && item < args.items; item += pairs) {
+      const VocabItem it = vocab_item(args, item);
+      for (int kb = it.kb0; kb < it.kb1; ++kb, ++g) {
+        const int slot = g % STAGES;
+        if (!mbar_wait_warp(&empty[slot], ((g / STAGES) & 1) ^ 1u, abort_flag)) { ok = false; break; }
+        uint8_t* dst = smem + slot * STAGE_BYTES;
+        const uint32_t bar = full0 + static_cast<uint32_t>(slot * sizeof(uint64_t));
+        if (elect_one()) {
           if (rank == 0) mbar_arrive_expect_tx(&full[slot], 2 * STAGE_BYTES);
-          const uint32_t bar = full0 + static_cast<uint32_t>(slot * sizeof(uint64_t));
 #pragma unroll
           for (int s = 0; s < KS; ++s) {   // (a step behind K's end is filled with zeros)
             const int k = (kb * KS + s) * BK;
@@ -245,16 +245,17 @@ __global__ void __launch_bounds__(vg::kThreads, 1)
             }
           }
         }
+        __syncwarp();
       }
-      if (*abort_flag) {
-        // no copy may still be writing shared memory when its CTA exits: the even CTA waits for its
-        // stages (both CTAs' bytes); the odd one, whose copies count there, gives its own, at most
-        // STAGES of them, a thousand times a copy's latency (and stays until the cluster's barrier)
-        if (rank == 0)
-          for (int j = (g > STAGES ? g - STAGES : 0); j < g; ++j) mbar_drain(&full[j % STAGES], (j / STAGES) & 1);
-        else
-          for (int i = 0; i < 2000; ++i) __nanosleep(1000);
-      }
+    }
+    if (lane == 0 && *abort_flag) {
+      // no copy may still be writing shared memory when its CTA exits: the even CTA waits for its
+      // stages (both CTAs' bytes); the odd one, whose copies count there, gives its own, at most
+      // STAGES of them, a thousand times a copy's latency (and stays until the cluster's barrier)
+      if (rank == 0)
+        for (int j = (g > STAGES ? g - STAGES : 0); j < g; ++j) mbar_drain(&full[j % STAGES], (j / STAGES) & 1);
+      else
+        for (int i = 0; i < 2000; ++i) __nanosleep(1000);
     }
   } else if (warp == kMmaWarp) {
     if (rank == 0) {
@@ -667,16 +668,16 @@ __global__ void __launch_bounds__(vn::kThreads, 1)
   narrow_begin(cta);
   const int u0 = unit_row(args.units, gridDim.x, blockIdx.x), u1 = unit_row(args.units, gridDim.x, blockIdx.x + 1);
 
-  if (warp == kTmaWarp) {
-    if (lane == 0) {
-      RingPos g;
-      bool ok = true;
-      for (int u = u0; ok && u < u1; u += 4) {
-        const int nu = min(4, u1 - u);
-        for (int kb = 0; kb < args.num_kb; ++kb, g.next(cta.stages)) {
-          const int slot = g.slot;
-          if (!mbar_wait(&cta.empty[slot], g.phase ^ 1u, cta.abort_flag)) { ok = false; break; }
-          uint8_t* dst = cta.stage + slot * cta.stage_bytes;
+  if (warp == kTmaWarp) {   // (warp-uniform, an elected lane issuing: one lane's branch takes hundreds of cycles a stage)
+    RingPos g;
+    bool ok = true;
+    for (int u = u0; ok && u < u1; u += 4) {
+      const int nu = min(4, u1 - u);
+      for (int kb = 0; kb < args.num_kb; ++kb, g.next(cta.stages)) {
+        const int slot = g.slot;
+        if (!mbar_wait_warp(&cta.empty[slot], g.phase ^ 1u, cta.abort_flag)) { ok = false; break; }
+        uint8_t* dst = cta.stage + slot * cta.stage_bytes;
+        if (elect_one()) {
           mbar_arrive_expect_tx(&cta.full[slot], KS * (nu * (kUnit * BK * 2) + args.n16 * (BK * 2)));
 #pragma unroll
           for (int s = 0; s < KS; ++s) {   // (a step behind h is filled with zeros)
@@ -690,9 +691,10 @@ __global__ void __launch_bounds__(vn::kThreads, 1)
             tma_load_2d(dst + A_BYTES + s * args.n16 * (BK * 2), &tmX, &cta.full[slot], x, 0);
           }
         }
+        __syncwarp();
       }
-      narrow_drain_copies(cta, g);
     }
+    if (lane == 0) narrow_drain_copies(cta, g);
   } else if (warp == kMmaWarp) {
     RingPos g;
     int n = 0;
@@ -811,13 +813,13 @@ __global__ void __launch_bounds__(vn::kThreads, 1)
   auto share_end = [&](int x) { return min(x1, (x / args.num_kb + 1) * args.num_kb); };
 
   if (warp == kTmaWarp) {
-    if (lane == 0) {
-      RingPos g;
-      int tile = x0 / args.num_kb, kb = x0 - tile * args.num_kb;
-      for (int x = x0; x < x1; ++x, g.next(cta.stages)) {
-        const int slot = g.slot;
-        if (!mbar_wait(&cta.empty[slot], g.phase ^ 1u, cta.abort_flag)) break;
-        uint8_t* dst = cta.stage + slot * cta.stage_bytes;
+    RingPos g;
+    int tile = x0 / args.num_kb, kb = x0 - tile * args.num_kb;
+    for (int x = x0; x < x1; ++x, g.next(cta.stages)) {
+      const int slot = g.slot;
+      if (!mbar_wait_warp(&cta.empty[slot], g.phase ^ 1u, cta.abort_flag)) break;
+      uint8_t* dst = cta.stage + slot * cta.stage_bytes;
+      if (elect_one()) {
         mbar_arrive_expect_tx(&cta.full[slot], cta.stage_bytes);
 #pragma unroll
         for (int s = 0; s < KS; ++s) {   // (a step behind ldp is filled with zeros)
@@ -826,13 +828,14 @@ __global__ void __launch_bounds__(vn::kThreads, 1)
           tma_load_2d(dst + s * A_ATOM + 8192, &tmW, &cta.full[slot], tile * BM + 64, k);
           tma_load_2d(dst + A_BYTES + s * args.n16 * (BK * 2), &tmG, &cta.full[slot], k, 0);
         }
-        if (++kb == args.num_kb) {
-          kb = 0;
-          ++tile;
-        }
       }
-      narrow_drain_copies(cta, g);
+      __syncwarp();
+      if (++kb == args.num_kb) {
+        kb = 0;
+        ++tile;
+      }
     }
+    if (lane == 0) narrow_drain_copies(cta, g);
   } else if (warp == kMmaWarp) {
     RingPos g;
     int n = 0;
