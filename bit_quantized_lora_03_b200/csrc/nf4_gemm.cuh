@@ -53,15 +53,19 @@ constexpr int P_BYTES = BNH * BK / 2;      // 4 KB of packed codes
 constexpr int P_STAGES = 8;                // their own ring, filled by a warp of its own: codes are read into
                                            // registers and their slot is free long before the step's MMAs
 constexpr int kWorkWarps = 8;              // warps 0-7: dequant producers, then epilogue
-constexpr int kGroupWarps = kWorkWarps / 2;  // producers of one stage: warps 0-3 of the even K-steps,
-                                             // 4-7 of the odd ones
+constexpr int kGroupWarps = 4;             // producers of one stage; the groups take K-steps in turn: warps
+                                           // 0-3, 4-7, and with kThreadsFew 11-14 (which only produce)
 constexpr int kTmaWarp = 8;
 constexpr int kMmaWarp = 9;                // even CTA: MMA issuer
 constexpr int kCodeWarp = 10;              // TMA of the packed codes
 constexpr int kThreads = 11 * 32;
+constexpr int kThreadsFew = 15 * 32;       // for 256 tokens or fewer: a step of half the products leaves two groups
+                                           // behind (16 tokens, 8192 x 8192: 38.7 -> 34.4 us; at 4096 tokens a
+                                           // third one costs 0.7%)
+inline int nf4_gemm_threads(int64_t tokens) { return tokens <= PAIR_M / 2 ? kThreadsFew : kThreads; }
+
 constexpr int kTmemCols = 512;
 constexpr int kEpiZTile = kWorkWarps * 8192;   // the staging tiles of Z lie behind those of Y
-static_assert(P_STAGES % 2 == 0, "a code slot belongs to one producer group");
 static_assert(2 * kEpiZTile <= STAGES * (A_BYTES + B_BYTES), "staging tiles in the drained stage buffers");
 
 constexpr size_t nf4_gemm_smem_bytes() {
@@ -106,7 +110,7 @@ __device__ __forceinline__ void mbar_drain(uint64_t* bar, uint32_t parity) {
 }
 
 template <bool kBwd, int kEpi = kEpiNone>
-__global__ void __launch_bounds__(tc::kThreads, 1)
+__global__ void __launch_bounds__(tc::kThreadsFew, 1)
     nf4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmP,
                     const __grid_constant__ CUtensorMap tmA2,
                     const __grid_constant__ CUtensorMap tmB2,
@@ -299,15 +303,16 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
   } else {
     // ---------------- warps 0-7: dequant producers (a 64-weight block per thread per stage: 128
     // blocks of this CTA's 128 columns), then the epilogue -----------------------------------
-    // Two groups of four warps take alternate K-steps: a step's chain of waits, table, selects and
+    // Groups of four warps take K-steps in turn: a step's chain of waits, table, selects and
     // stores is longer than its MMAs, so that one group alone, or all eight warps on every step,
     // would set the pace (and a thread builds a block's table once, not two threads each).
     uint64_t lv2[8];                 // the 16 fp32 levels as pairs (2i low, 2i+1 high)
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       asm("mov.b64 %0, {%1, %2};" : "=l"(lv2[i]) : "f"(args.tab.level[2 * i]), "f"(args.tab.level[2 * i + 1]));
-    const int group = warp / kGroupWarps;
-    const int blk = threadIdx.x & (kGroupWarps * 32 - 1);   // 0..127
+    const int groups = blockDim.x == kThreadsFew ? 3 : 2;
+    const int group = warp < kWorkWarps ? warp / kGroupWarps : 2;
+    const int blk = (threadIdx.x + (warp < kWorkWarps ? 0 : 32)) & (kGroupWarps * 32 - 1);   // 0..127
     const int64_t nblk_row = args.h / kBlock;
     int64_t qbase, qstep;       // q8 index of this thread's block at weight K-step kb: qbase + kb*qstep
     int out_off, pk_off, swz;
@@ -339,7 +344,7 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
     float sr[kPf];
 #pragma unroll
     for (int j = 0; j < kPf; ++j) {
-      const int i = 2 * j + group;
+      const int i = groups * j + group;
       qr[j] = 0u;
       sr[j] = 0.f;
       if (valid && i < nk) {
@@ -349,18 +354,18 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
       }
     }
     bool ok = true;
-    for (int i0 = group; i0 < total && ok; i0 += 2 * kPf) {
+    for (int i0 = group; i0 < total && ok; i0 += groups * kPf) {
 #pragma unroll
       for (int j = 0; j < kPf; ++j) {
-        const int i = i0 + 2 * j;
+        const int i = i0 + groups * j;
         if (i >= total || !ok) break;
         const int slot = i % STAGES;
         const uint32_t ph = (i / STAGES) & 1;
         if (i < nk) {
           // codes and table first: they do not depend on the operand slot's MMAs
           const float k = __fmul_rn(static_cast<float>(qr[j]), sr[j]);
-          if (valid && i + 2 * kPf < nk) {
-            const int64_t qi = qbase + static_cast<int64_t>(kb0 + i + 2 * kPf) * qstep;
+          if (valid && i + groups * kPf < nk) {
+            const int64_t qi = qbase + static_cast<int64_t>(kb0 + i + groups * kPf) * qstep;
             qr[j] = __ldg(args.q8 + qi);
             sr[j] = __ldg(args.s2 + (qi >> 8));
           }
@@ -403,6 +408,7 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
     // The fused epilogue walks 16 columns at a time in a loop that is not unrolled: its code runs a few
     // times per CTA, and 64 columns of straight-line code per activation took longer to fetch than to
     // execute. Bias and residual run one step ahead, the first ones ahead of the last products.
+    const bool epi_warp = warp < kWorkWarps;
     const int epi_row0 = mrow + (warp >> 2) * 256 + (warp & 3) * 32, epi_row = epi_row0 + lane;
     uint4 rq[2], bq[2];
     auto epi_load = [&](int col) {
@@ -413,8 +419,8 @@ __global__ void __launch_bounds__(tc::kThreads, 1)
           rq[k] = ldg_vec(args.epi.residual, ((static_cast<int64_t>(epi_row) * args.N + col) >> 3) + k);
       }
     };
-    if (kEpi == kEpiFused && epi_row0 < args.M) epi_load(n0);
-    const bool done = mbar_wait_warp(acc_full, 0, abort_flag);
+    if (kEpi == kEpiFused && epi_warp && epi_row0 < args.M) epi_load(n0);
+    const bool done = epi_warp && mbar_wait_warp(acc_full, 0, abort_flag);
     tc_fence_after();
     if (__all_sync(0xFFFFFFFFu, done && !*abort_flag)) {
       if (args.addend) pdl_wait();

@@ -438,13 +438,13 @@ GemvWs carve_gemv(void* base, int64_t t, int64_t o, int64_t r) {
 constexpr int64_t kGemvMaxTokens = 16;
 
 // Shares of K of the linear with the fused epilogue on the tcgen05 path: its tiles of 512 tokens x 256
-// outputs leave most of the card idle for a few hundred tokens. A K-step takes about 0.6 us (0.47 with
+// outputs leave most of the card idle for a few hundred tokens. A K-step takes about 0.6 us (0.43 with
 // one accumulator) and a share 11 us (7) besides, a round of pairs as long as one share; the shares cost
 // their fp32 traffic at some 5 TB/s and another launch. 4096 -> 4096: 17 tokens 64 -> 18 us with the join;
 // 11008 -> 4096: 777 tokens 150 -> 83 us. Planned for 148 SMs, so that the workspace is a host function.
 int epilogue_shares(int64_t t, int64_t h, int64_t o) {
   const int64_t tiles = (t + 511) / 512 * ((o + 255) / 256), kb = h / 64, pairs = 148 / 2;
-  const double step = t > 256 ? 0.6 : 0.47, fixed = t > 256 ? 11.0 : 7.0;
+  const double step = t > 256 ? 0.6 : 0.43, fixed = t > 256 ? 11.0 : 7.0;
   int best = 1;
   double cost = 0.0;
   for (int s = 1; s <= 16 && kb / s >= 4; ++s) {
@@ -619,7 +619,7 @@ int launch_nf4_gemm(const CUtensorMap& mA, const CUtensorMap& mP, const CUtensor
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(2 * ((ncols + tc::BN - 1) / tc::BN)),
                      static_cast<unsigned>((t + tc::PAIR_M - 1) / tc::PAIR_M), static_cast<unsigned>(shares));
-  cfg.blockDim = dim3(tc::kThreads, 1, 1);
+  cfg.blockDim = dim3(static_cast<unsigned>(tc::nf4_gemm_threads(t)), 1, 1);
   cfg.dynamicSmemBytes = tc::nf4_gemm_smem_bytes();
   cfg.stream = st;
   // always launched right after the kernel that produces its LoRA operand (sT or sU): it
