@@ -393,8 +393,8 @@ int qlora_linear_fwd_epilogue(const uint16_t* X, int64_t t, const nf4_weight* W,
 
 size_t qlora_fwd_epilogue_workspace_bytes(int64_t t, int64_t h, int64_t o, int64_t r) {
   const size_t base = qlora_fwd_workspace_bytes(t, h, o, r);
-  if (!base || !epilogue_uses_gemm(t, h, o)) return base;
-  const int shares = epilogue_shares(t, h, o);
+  if (!base || !epilogue_uses_gemm(t, h, o, r)) return base;
+  const int shares = plan_epilogue(t, h, o).shares;
   return lora_region_bytes(t, r) + (shares > 1 ? static_cast<size_t>(shares) * t * o * 4 : 0);
 }
 

@@ -442,30 +442,36 @@ constexpr int64_t kGemvMaxTokens = 16;
 // one accumulator) and a share 11 us (7) besides, a round of pairs as long as one share; the shares cost
 // their fp32 traffic at some 5 TB/s and another launch. 4096 -> 4096: 17 tokens 64 -> 18 us with the join;
 // 11008 -> 4096: 777 tokens 150 -> 83 us. Planned for 148 SMs, so that the workspace is a host function.
-int epilogue_shares(int64_t t, int64_t h, int64_t o) {
+struct EpiloguePlan {
+  int shares;
+  double us;   // of the GEMM and the join
+};
+EpiloguePlan plan_epilogue(int64_t t, int64_t h, int64_t o) {
   const int64_t tiles = (t + 511) / 512 * ((o + 255) / 256), kb = h / 64, pairs = 148 / 2;
   const double step = t > 256 ? 0.6 : 0.43, fixed = t > 256 ? 11.0 : 7.0;
-  int best = 1;
-  double cost = 0.0;
+  EpiloguePlan best{};
   for (int s = 1; s <= 16 && kb / s >= 4; ++s) {
     const int64_t per = (kb + s - 1) / s;
     if (s > 1 && per * (s - 1) >= kb) continue;   // a share would be empty
     const double c = static_cast<double>((tiles * s + pairs - 1) / pairs) * (per * step + fixed) +
                      (s > 1 ? 8.0 * s * t * o / 5e6 + 4.0 : 0.0);
-    if (s == 1 || c < cost) {
-      cost = c;
-      best = s;
-    }
+    if (!best.shares || c < best.us) best = {s, c};
   }
+  if (!best.shares) best.shares = 1;   // (fewer than four K-steps)
   return best;
 }
 
 // Whether the linear with the fused epilogue takes the tcgen05 path: above the GEMV's tokens, and from 9
-// tokens (the GEMV's second token tile) where the weight is large and its shares fill the card. 16 tokens,
-// 8192 -> 8192: GEMV 63 us, this 42; 11008 -> 4096: 58 and 33; 2048 -> 8192: 36 and 22; with one share
-// 4096 -> 11008: 41 and 46.
-bool epilogue_uses_gemm(int64_t t, int64_t h, int64_t o) {
-  return t > kGemvMaxTokens || (t > 8 && h * o >= (int64_t(1) << 23) && epilogue_shares(t, h, o) > 1);
+// tokens (the GEMV's second token tile) for a large weight where it is the shorter one by the estimates, in
+// us: the GEMM's and 6 for its rank-r product, against 20, 0.24 per rank and 0.36 per million weights for the
+// GEMV. GEMV and GEMM measured at 16 tokens, rank 64: 8192 -> 8192 63, 40; 11008 -> 4096 58, 31; 4096 -> 16384
+// 66, 42; 1024 -> 11008 43, 23; 8192 -> 10240 73, 56; 8192 -> 28672 126, 127 (9 tokens: 113, 127); rank 16:
+// 2048 -> 16384 39, 28; 4096 -> 11008 42, 39 (9 tokens: 37, 39); 1024 -> 20480 37, 38.
+bool epilogue_uses_gemm(int64_t t, int64_t h, int64_t o, int64_t r) {
+  if (t > kGemvMaxTokens) return true;
+  const double weights = static_cast<double>(h) * static_cast<double>(o);
+  return t > 8 && weights >= (1 << 23) &&
+         plan_epilogue(t, h, o).us + 6.0 < 20.0 + 0.24 * static_cast<double>(r) + 0.36e-6 * weights;
 }
 
 // ------------------------------------------------------------------------------------------
@@ -739,7 +745,7 @@ int fwd_core(const uint16_t* X, const uint16_t* Xl, int64_t t, const nf4_weight*
   if ((rc = current_device(&dev))) return rc;
   const int64_t h = W->in_features, o = W->out_features;
   const int sms = sm_count(dev);
-  if (epi ? !epilogue_uses_gemm(t, h, o) : t <= kGemvMaxTokens) {
+  if (epi ? !epilogue_uses_gemm(t, h, o, r) : t <= kGemvMaxTokens) {
     // partial sums of Xl.L1 (+ zeroed sums and counters), then the GEMV, which forms
     // sT = bf16(s . Xl.L1) and finishes Y
     GemvWs gw = carve_gemv(workspace, t, o, r);
@@ -827,7 +833,7 @@ int fwd_core(const uint16_t* X, const uint16_t* Xl, int64_t t, const nf4_weight*
   ga.tab = device_table();
   if (epi) {
     ga.epi = *epi;
-    const int shares = epilogue_shares(t, h, o);
+    const int shares = plan_epilogue(t, h, o).shares;
     if (shares == 1) return launch_nf4_gemm<false, kEpiFused>(mA, mP, mA2, mB2, ga, t, o, st, prof::kGemmFwd);
     float* part = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(workspace) + lora_region_bytes(t, r));
     ga.kb_per_split = (ga.num_kb + shares - 1) / shares;

@@ -44,6 +44,8 @@ CASES = [  # t, h, o, r, act, bias, residual, Z kept
     # K split over the card: one and two accumulators, shares of unequal length, two row tiles
     (23, 4096, 512, 64, "silu", True, True, True), (300, 2112, 320, 16, "gelu", True, True, False),
     (700, 1984, 192, 48, "none", False, True, True), (12, 8192, 4096, 32, "silu", True, True, True), (129, 11008, 256, 80, "relu", True, False, False),
+    # a large weight for 9 to 16 tokens, K whole
+    (9, 1024, 8256, 48, "gelu", True, True, True),
 ]
 
 
