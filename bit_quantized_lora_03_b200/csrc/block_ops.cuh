@@ -103,10 +103,8 @@ VocabPlan plan_vocab(int64_t t, int64_t h, int64_t v, bool stats, bool grad) {
                                   vn::tokens16(static_cast<int>(t)) * 4
                             : static_cast<size_t>(kVocabMaxParts) * vg::BM * vg::BN * 4;
   }
-  if (stats) {
-    p.stats_bytes = align256(static_cast<size_t>(p.run) * p.pieces * 8);
-    p.row_bytes = align256(static_cast<size_t>(p.run) * 4);
-  }
+  if (stats) p.stats_bytes = align256(static_cast<size_t>(p.run) * p.pieces * 8);
+  p.row_bytes = align256(static_cast<size_t>(p.run) * 4);
   return p;
 }
 
@@ -261,6 +259,7 @@ int vocab_core(const VocabCall& c, void* workspace, cudaStream_t st) {
     a.lse = c.lse;
     a.dloss = c.dloss;
     a.dlse = c.dlse;
+    a.target_factor = target_factor;
     a.redo = stats ? redo : nullptr;
     a.g = g;
     a.part = part;
@@ -291,10 +290,10 @@ int vocab_core(const VocabCall& c, void* workspace, cudaStream_t st) {
     f.N = d.h;
     f.targets = c.targets;
     f.W = c.W;
+    f.target_factor = target_factor;
     if (stats) {
       f.redo = redo;
       f.factor = factor;
-      f.target_factor = target_factor;
     }
     prof::Scope ps(prof::kVocabRows, st);
     vocab_narrow_join_kernel<<<dim3(static_cast<unsigned>(d.tiles), static_cast<unsigned>((c.t + 1) / 2)), 256, 0, st>>>(
@@ -324,6 +323,7 @@ int vocab_core(const VocabCall& c, void* workspace, cudaStream_t st) {
     if (grad) {
       a.dloss = c.dloss + i0;
       a.dlse = c.dlse ? c.dlse + i0 : nullptr;
+      a.target_factor = target_factor;
     }
     if (stats) {
       if (grad) {
@@ -341,10 +341,10 @@ int vocab_core(const VocabCall& c, void* workspace, cudaStream_t st) {
     VocabGemmArgs d = plan_vocab_gemm(n, c.h, c.v, true, pairs);
     d.targets = a.targets;
     d.W = c.W;
+    d.target_factor = target_factor;
     if (stats) {
       d.redo = redo;
       d.factor = factor;
-      d.target_factor = target_factor;
     }
     if ((rc = launch_vocab_gemm<kVocabGrad>(mG, mWmn, mD, mPart, d, pairs, st))) return rc;
     if (d.splits > 1) {

@@ -10,7 +10,7 @@
 //   kVocabStats   a token's reference point (its maximum) and sum of exp(l - reference) over the piece,
 //                 and the target's logit
 //   kVocabScaled  the same with the target's logit as the reference, and exp(l - reference) in bf16
-//   kVocabProb    g in bf16, lse being known
+//   kVocabProb    g in bf16 but for the target's term, lse being known
 //   kVocabGrad    (the second product, dX = g.W) dX in bf16, or fp32 partial tiles of a split K
 // Only statistics leave the first kernel: 8 bytes per token and piece instead of 512. The backward
 // holds g (or the scaled exponentials) of a bounded run of tokens at a time in the workspace.
@@ -21,10 +21,11 @@
 // when a piece's logits are, floating point keeps its relative precision whatever its scale, and the
 // row's factor dloss.exp(l[y] - lse) is applied to the finished dX. The logits l[y] come first, from a
 // kernel of their own (t dot products). The target's own term is left out of g and added in fp32 as
-// dloss.(exp(-loss) - 1).W[y], so that a confident token's small difference is not one of two rounded
-// numbers. Only where some logit exceeds its row's target by more than 60 (a loss above 60) could the
-// sums overflow: the piece then raises a flag, and kVocabProb runs again over the run with its lse
-// (otherwise that launch returns at once).
+// (a.p[y] - b).W[y] (with one call dloss.(exp(-loss) - 1).W[y]), so that a confident token's small
+// difference is not one of two rounded numbers and the largest term is not rounded to bf16. Only where
+// some logit exceeds its row's target by more than 60 (a loss above 60) could the sums overflow: the piece
+// then raises a flag, and kVocabProb runs again over the run with its lse (otherwise that launch returns
+// at once).
 //
 // Logits are accumulated 512 inputs at a time in tensor memory and summed in the epilogue's registers.
 // The tensor core truncates its fp32 sum after every 16 inputs: over 4096 (8192) inputs a logit then
@@ -89,8 +90,8 @@ struct VocabGemmArgs {
   const float* dlse;     // or NULL
   unsigned* redo;        // kVocabScaled: raised by rows it cannot serve. kVocabProb: NULL, or the flag
                          // without which there is nothing to do. kVocabGrad: see row_factor
-  const float* factor;   // kVocabGrad: NULL, or a row's factor and its target's
-  const float* target_factor;
+  const float* factor;   // kVocabGrad: NULL, or the rows' factors
+  float* target_factor;  // kVocabProb writes, kVocabGrad reads: the factors of the targets' W
   const uint16_t* W;
 };
 
@@ -118,15 +119,13 @@ __device__ __forceinline__ VocabItem vocab_item(const VocabGemmArgs& a, int item
   return it;
 }
 
-// dX from the second product: a row's factor times it, plus its target's factor times W[target].
-// Without factors, or after kVocabProb ran again (g is then complete), the product itself.
+// dX from the second product: a row's factor times it, plus its target's factor times W[target]. The row's
+// factor is 1 without factors, or after kVocabProb ran again (g is then complete).
 struct RowFactor {
   float f, ft;
   const uint16_t* w;   // the target's row of W, or NULL
-  bool plain;
   // eight columns from `col` on (col < the row's length, a multiple of 8)
   __device__ __forceinline__ void apply(float (&v)[8], int col) const {
-    if (plain) return;
     float t[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (w) unpack8(ldg_vec(w, col >> 3), t);
 #pragma unroll
@@ -135,11 +134,10 @@ struct RowFactor {
 };
 __device__ __forceinline__ RowFactor row_factor(const VocabGemmArgs& a, int row) {
   RowFactor r;
-  r.plain = !a.factor || *a.redo != 0u;
   r.f = r.ft = 0.f;
   r.w = nullptr;
-  if (!r.plain && row >= 0) {
-    r.f = a.factor[row];
+  if (row >= 0) {
+    r.f = !a.factor || *a.redo != 0u ? 1.f : a.factor[row];
     r.ft = a.target_factor[row];
     if (r.ft != 0.f) r.w = a.W + a.targets[row] * a.N;   // (counted: inside the vocabulary)
   }
@@ -417,10 +415,15 @@ __global__ void __launch_bounds__(vg::kThreads, 1)
         // a row that counts for nothing is zero whatever its logits are
 #pragma unroll
         for (int e = 0; e < PIECE; ++e) s[e] = a != 0.f ? a * ex2(fmaf(s[e], kLog2e, nl)) : 0.f;
+        float ft = 0.f;
         if (any_target) {
 #pragma unroll
-          for (int e = 0; e < PIECE; ++e) s[e] -= e == tcol ? b : 0.f;
+          for (int e = 0; e < PIECE; ++e) {
+            ft = e == tcol ? s[e] - b : ft;
+            s[e] = e == tcol ? 0.f : s[e];
+          }
         }
+        if (rok && (tcol >= 0 || (!counted && n0 == 0))) args.target_factor[row] = ft;
       } else {
         constexpr bool kScaled = kMode == kVocabScaled;
         if (any_target) {
@@ -518,6 +521,7 @@ struct VocabNarrowArgs {
   const float* lse;
   const float* dloss;
   const float* dlse;
+  float* target_factor;
   unsigned* redo;
   uint16_t* g;           // t x ldp
   float* part;           // the gradient's partial tiles: [slot][token][128]
@@ -748,7 +752,12 @@ __global__ void __launch_bounds__(vn::kThreads, 1)
               const float a = t_a[c + j];
               // a row that counts for nothing is zero whatever its logits are
               p[j] = wok && a != 0.f ? a * ex2(fmaf(v[j], vg::kLog2e, t_ref[c + j])) : 0.f;
-              if (word == t_word[c + j]) p[j] -= t_b[c + j];
+              const int w = t_word[c + j];
+              if (word == w) {
+                args.target_factor[c + j] = p[j] - t_b[c + j];
+                p[j] = 0.f;
+              }
+              if (w < 0 && word == 0 && c + j < args.t) args.target_factor[c + j] = 0.f;
             }
           } else {
             constexpr bool kScaled = kMode == kVocabScaled;
@@ -1004,7 +1013,7 @@ __global__ void __launch_bounds__(256)
     s += __ldcg(part + (static_cast<int64_t>(i + tile) * a.n16 + tok) * vn::BM + col);
   const RowFactor rf = row_factor(f, tok);
   const int hc = tile * vn::BM + col;
-  if (!rf.plain) s = rf.f == 0.f ? 0.f : fmaf(s, rf.f, rf.w ? rf.ft * bf16_bits_to_float(rf.w[hc]) : 0.f);
+  s = rf.f == 0.f ? 0.f : fmaf(s, rf.f, rf.w ? rf.ft * bf16_bits_to_float(rf.w[hc]) : 0.f);
   dX[static_cast<int64_t>(tok) * a.h + hc] = __bfloat16_as_ushort(__float2bfloat16_rn(s));
 }
 
