@@ -288,14 +288,15 @@ template <int NT, bool kEpi>
 __device__ __forceinline__ void gemv_finish_tile(const GemvArgs& a, const uint16_t* sts,
                                                  int64_t tile, int lane) {
   const int64_t row = tile * gv::kTileRows + lane;
-  // the operands that do not depend on the sums go in flight with them: one latency, not three
+  // the operands that do not depend on the sums go in flight with them: one latency, not three (for up to
+  // 8 tokens; the registers of 16 are full)
   float l2[8];
   auto load_l2 = [&](int c0) {   // r % 16 == 0: eight loads in flight per lane
 #pragma unroll
     for (int j = 0; j < 8; ++j)
       l2[j] = bf16_bits_to_float(__ldg(a.L2 + static_cast<int64_t>(c0 + j) * a.o + row));
   };
-  load_l2(0);
+  if (NT == 1) load_l2(0);
   const float bias = kEpi && a.epi.bias ? bf16_bits_to_float(__ldg(a.epi.bias + row)) : 0.f;
   float y[NT * 8];
 #pragma unroll
@@ -303,9 +304,10 @@ __device__ __forceinline__ void gemv_finish_tile(const GemvArgs& a, const uint16
     y[n] = n < a.t ? __ldcg(a.Y32 + static_cast<int64_t>(n) * a.o + row) : 0.f;
   for (int c0 = 0; c0 < a.r; c0 += 8) {
     float cur[8];
+    if (NT != 1) load_l2(c0);
 #pragma unroll
     for (int j = 0; j < 8; ++j) cur[j] = l2[j];
-    if (c0 + 8 < a.r) load_l2(c0 + 8);
+    if (NT == 1 && c0 + 8 < a.r) load_l2(c0 + 8);
 #pragma unroll
     for (int j = 0; j < 8; ++j)
 #pragma unroll
@@ -410,33 +412,21 @@ __global__ void __launch_bounds__(gv::kThreads, 1)
       table[i] = make_float2(args.tab.level[e >> 4], args.tab.level[e & 15]);
     }
   }
-  // sT = bf16(s . X.L1) from the LoRA-down kernel's partial sums, once per CTA, by all its warps.
-  // That kernel is launched just before this one, which may start early: wait for its completion
-  // and memory first. Nothing needs either before a warp's first sums are added (to a buffer that
-  // kernel zeroes). For 9 to 16 tokens, where it takes 12 us (8192 inputs, rank 64), every warp comes
-  // here only then, most of its work behind it; for up to 8 it is done by the time the table is, and
-  // joining later would only lengthen the end (24.7 against 26.7 us for one token, 4096 x 11008).
-  auto join_lora = [&]() {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    for (int i = threadIdx.x; i < args.t * args.r; i += kThreads) {
-      float v = 0.f;
+  // sT = bf16(s . X.L1) from the LoRA-down kernel's partial sums (launched just before this
+  // kernel, which may start early: wait for its completion and memory first). Joining them later, when a
+  // warp's first sums are due, only lengthens the end: 26.7 against 24.7 us for one token, 4096 x 11008,
+  // 45 against 38 for 16.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  for (int i = threadIdx.x; i < args.t * args.r; i += kThreads) {
+    float v = 0.f;
 #pragma unroll
-      for (int p = 0; p < kDownParts; ++p) v += __ldcg(args.Tpart + p * args.t * args.r + i);
-      const uint16_t b = __bfloat16_as_ushort(__float2bfloat16_rn(args.s * v));
-      sts[(i / args.r) * kMaxRank + i % args.r] = b;
-      if (blockIdx.x == 0 && args.sT_out) args.sT_out[i] = b;
-    }
-    __syncthreads();
-  };
-  bool joined = NT == 1;
-  if (joined)
-    join_lora();
-  else
-    __syncthreads();
-  if (nrun <= 0) {
-    if (!joined) join_lora();
-    return;
+    for (int p = 0; p < kDownParts; ++p) v += __ldcg(args.Tpart + p * args.t * args.r + i);
+    const uint16_t b = __bfloat16_as_ushort(__float2bfloat16_rn(args.s * v));
+    sts[(i / args.r) * kMaxRank + i % args.r] = b;
+    if (blockIdx.x == 0 && args.sT_out) args.sT_out[i] = b;
   }
+  __syncthreads();
+  if (nrun <= 0) return;
 
   const uint32_t lane_slot = tab + static_cast<uint32_t>(lane) * 8u;
   float acc[2][NT][4];
@@ -468,10 +458,7 @@ __global__ void __launch_bounds__(gv::kThreads, 1)
       }
     const int64_t row0 = cur.tile * kTileRows;
     for (int u = cur.u0; u < cur.u1; ++u) {
-      if (!mbar_wait_warp(&bars[e], ph, &abort_flag)) {
-        if (!joined) join_lora();
-        return;
-      }
+      if (!mbar_wait_warp(&bars[e], ph, &abort_flag)) return;
       GemvCodes cc;
       gemv_read_codes(cc, slot + kSlotCodes + e * kUnitBytes, g, q);
       __syncwarp();  // every lane has read the entry before it is refilled
@@ -520,8 +507,6 @@ __global__ void __launch_bounds__(gv::kThreads, 1)
     }
     tile_units += cur.u1 - cur.u0;
     if (nxt.u0 == nxt.u1 || nxt.tile != cur.tile) {
-      if (!joined) join_lora();
-      joined = true;
       // add the tile's sums, then count its units; the warp that completes the tile
       // finishes it (the fence makes this warp's sums visible before its count)
       gemv_flush<NT>(acc, args, cur.tile, g, q);

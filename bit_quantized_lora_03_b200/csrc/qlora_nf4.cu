@@ -463,15 +463,17 @@ EpiloguePlan plan_epilogue(int64_t t, int64_t h, int64_t o) {
 
 // Whether the linear with the fused epilogue takes the tcgen05 path: above the GEMV's tokens, and from 9
 // tokens (the GEMV's second token tile) for a large weight where it is the shorter one by the estimates, in
-// us: the GEMM's and 6 for its rank-r product, against 20, 0.24 per rank and 0.36 per million weights for the
-// GEMV. GEMV and GEMM measured at 16 tokens, rank 64: 8192 -> 8192 63, 40; 11008 -> 4096 58, 31; 4096 -> 16384
-// 66, 42; 1024 -> 11008 43, 23; 8192 -> 10240 73, 56; 8192 -> 28672 126, 127 (9 tokens: 113, 127); rank 16:
-// 2048 -> 16384 39, 28; 4096 -> 11008 42, 39 (9 tokens: 37, 39); 1024 -> 20480 37, 38.
+// us: the GEMM's and what its rank-r product adds, against the GEMV's (a fit over the shapes below and some
+// more). GEMV and GEMM measured at 16 tokens, rank 64: 8192 -> 8192 55, 40; 11008 -> 4096 45, 31; 22016 -> 8192
+// 100, 79; 4096 -> 16384 53, 42; 1024 -> 11008 37, 24; 8192 -> 10240 61, 56; 8192 -> 22016 96, 99; 8192 -> 28672
+// 113, 127; rank 16: 2048 -> 16384 32, 28; 8192 -> 8192 43, 40; 4096 -> 11008 33, 40; 1024 -> 20480 33, 38.
 bool epilogue_uses_gemm(int64_t t, int64_t h, int64_t o, int64_t r) {
   if (t > kGemvMaxTokens) return true;
   const double weights = static_cast<double>(h) * static_cast<double>(o);
-  return t > 8 && weights >= (1 << 23) &&
-         plan_epilogue(t, h, o).us + 6.0 < 20.0 + 0.24 * static_cast<double>(r) + 0.36e-6 * weights;
+  if (t <= 8 || weights < (1 << 23)) return false;
+  const EpiloguePlan p = plan_epilogue(t, h, o);
+  return p.us + (p.shares > 1 ? 1.0 : 6.0) <
+         15.0 + 0.1 * static_cast<double>(r) + 0.25e-3 * static_cast<double>(o) + 0.37e-6 * weights;
 }
 
 // ------------------------------------------------------------------------------------------
