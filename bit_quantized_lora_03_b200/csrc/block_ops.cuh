@@ -26,13 +26,12 @@ int epilogue_runs(int64_t t, int64_t o, int sms, int ctas) {
   return static_cast<int>(runs);
 }
 
-cudaError_t launch_finish(const float* part_pre, const float* part_post, const float* part_gate, float* dw_pre,
+int launch_finish(const float* part_pre, const float* part_post, const float* part_gate, float* dw_pre,
                           float* dw_post, float* dgate, int t, int h, int rows_per_gate, int parts, int units,
                           int grid_y, cudaStream_t st) {
   dim3 grid(static_cast<unsigned>((h + nr::kFinishCols - 1) / nr::kFinishCols), static_cast<unsigned>(grid_y));
-  norm_residual_finish_kernel<<<grid, nr::kFinishWarps * 32, 0, st>>>(
-      part_pre, part_post, part_gate, dw_pre, dw_post, dgate, t, h, rows_per_gate, parts, units);
-  return cudaGetLastError();
+  return launch_after(norm_residual_finish_kernel, grid, nr::kFinishWarps * 32, st, part_pre, part_post, part_gate,
+                      dw_pre, dw_post, dgate, t, h, rows_per_gate, parts, units);
 }
 
 // ------------------------------------------------------------------------------------------
@@ -239,8 +238,8 @@ int vocab_core(const VocabCall& c, void* workspace, cudaStream_t st) {
     }
     prof::Scope ps(prof::kVocabRows, st);
     const bool few = n <= kFewRows;
-    (few ? vocab_rows_kernel<8> : vocab_rows_kernel<1>)<<<static_cast<unsigned>(few ? n : (n + 7) / 8), 256, 0, st>>>(r);
-    return launch_status();
+    return launch_after(few ? vocab_rows_kernel<8> : vocab_rows_kernel<1>,
+                        dim3(static_cast<unsigned>(few ? n : (n + 7) / 8)), 256, st, r);
   };
   if (p.narrow) {
     VocabNarrowArgs a{};
@@ -296,9 +295,9 @@ int vocab_core(const VocabCall& c, void* workspace, cudaStream_t st) {
       f.factor = factor;
     }
     prof::Scope ps(prof::kVocabRows, st);
-    vocab_narrow_join_kernel<<<dim3(static_cast<unsigned>(d.tiles), static_cast<unsigned>((c.t + 1) / 2)), 256, 0, st>>>(
-        part, c.dX, d, f, gctas);
-    return launch_status();
+    return launch_after(vocab_narrow_join_kernel,
+                        dim3(static_cast<unsigned>(d.tiles), static_cast<unsigned>((c.t + 1) / 2)), 256, st, part, c.dX, d,
+                        f, gctas);
   }
   CUtensorMap mWk, mWmn, mPart;
   if (!map_bf16(&mWk, c.W, c.h, c.v, 64, 128) || !map_bf16(&mWmn, c.W, c.h, c.v, 64, 64)) return QLORA_ERR_CUDA;
@@ -349,8 +348,9 @@ int vocab_core(const VocabCall& c, void* workspace, cudaStream_t st) {
     if ((rc = launch_vocab_gemm<kVocabGrad>(mG, mWmn, mD, mPart, d, pairs, st))) return rc;
     if (d.splits > 1) {
       const int tiles = d.m_tiles * d.n_tiles - d.whole;
-      vocab_join_kernel<<<dim3(static_cast<unsigned>(tiles), vg::BM / 8), 256, 0, st>>>(part, c.dX + i0 * c.h, d);
-      if ((rc = launch_status())) return rc;
+      if ((rc = launch_after(vocab_join_kernel, dim3(static_cast<unsigned>(tiles), vg::BM / 8), 256, st, part,
+                             c.dX + i0 * c.h, d)))
+        return rc;
     }
   }
   return QLORA_OK;
@@ -435,11 +435,8 @@ int qlora_epilogue_bwd(const uint16_t* dY, const uint16_t* Z, int64_t t, int64_t
     }
   }
   if ((rc = launch_status())) return rc;
-  if (dbias && runs > 1 &&
-      launch_finish(a.part, nullptr, nullptr, dbias, nullptr, nullptr, static_cast<int>(t), a.o, 1, runs, 0, 1,
-                    st) != cudaSuccess)
-    return QLORA_ERR_CUDA;
-  return QLORA_OK;
+  if (!dbias || runs == 1) return QLORA_OK;
+  return launch_finish(a.part, nullptr, nullptr, dbias, nullptr, nullptr, static_cast<int>(t), a.o, 1, runs, 0, 1, st);
 }
 
 int qlora_norm_residual_fwd(const uint16_t* x, const uint16_t* y, int64_t t, int64_t h, const uint16_t* w_post,
@@ -582,10 +579,8 @@ int qlora_norm_residual_bwd(const uint16_t* dx_out, const uint16_t* dn, const ui
   float* pre = pl.ctas > 1 ? dw_pre : nullptr;
   float* post = pl.ctas > 1 ? dw_post : nullptr;
   if (!pre && !post && !gate_blocks) return QLORA_OK;
-  if (launch_finish(a.part_pre, a.part_post, a.part_gate, pre, post, dgate, a.t, a.h, a.rows_per_gate, pl.ctas,
-                    pl.units, 2 + gate_blocks, st) != cudaSuccess)
-    return QLORA_ERR_CUDA;
-  return QLORA_OK;
+  return launch_finish(a.part_pre, a.part_post, a.part_gate, pre, post, dgate, a.t, a.h, a.rows_per_gate, pl.ctas,
+                       pl.units, 2 + gate_blocks, st);
 }
 
 size_t qlora_vocab_loss_fwd_workspace_bytes(int64_t t, int64_t h, int64_t v) {

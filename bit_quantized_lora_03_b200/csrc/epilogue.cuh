@@ -136,6 +136,7 @@ __global__ void __launch_bounds__(ep::kWarps * 32)
     epilogue_bwd_kernel(const EpilogueBwdArgs a) {
   using namespace ep;
   __shared__ float sh[kWarps][kCols];
+  pdl_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int nvec = a.o >> 3;
   const int v = blockIdx.x * (kCols / 8) + lane;

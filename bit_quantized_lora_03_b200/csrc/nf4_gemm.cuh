@@ -578,6 +578,7 @@ __global__ void __launch_bounds__(tc::kThreadsFew, 1)
 // row per thread.
 __global__ void __launch_bounds__(256)
     nf4_gemm_join_kernel(const float* part, int shares, uint16_t* Y, int64_t rows, int N, const EpilogueArgs epi) {
+  pdl_wait();
   const int64_t vec = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x, nvec = N >> 3;
   if (vec >= rows * nvec) return;
   float z[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};

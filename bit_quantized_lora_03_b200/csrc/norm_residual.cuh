@@ -365,6 +365,7 @@ template <bool kWarpRow, bool kWide, bool kAll = false>
 __global__ void __launch_bounds__(kWarpRow ? nr::kWarpRowThreads : (kWide ? 1024 : 512))
     norm_residual_bwd_kernel(const NormBwdArgs a) {
   constexpr int VPT = 2, S = nr::kBwdStages;
+  pdl_launch_dependents();
   extern __shared__ __align__(16) float4 dyn[];
   __shared__ float red[2 * 3 * 32];
   const int nthr = kWarpRow ? 32 : blockDim.x;
@@ -622,6 +623,7 @@ __global__ void __launch_bounds__(nr::kFinishWarps * 32)
   __shared__ float4 sh[nr::kFinishWarps][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int col = blockIdx.x * nr::kFinishCols + lane * 4;
+  pdl_wait();
   const bool cv = col < h;   // h % 8 == 0
   // out[col..] = the sum of rows [0, n) at `first`, and of the row at `extra` if there is one
   auto sum_rows = [&](const float* first, int n, const float* extra, float* out) {

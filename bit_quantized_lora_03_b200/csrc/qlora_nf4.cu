@@ -274,6 +274,27 @@ int launch_status() {
   return e == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
 }
 
+// A kernel that begins with pdl_wait(), launched so that its start overlaps the end of the kernel before it on
+// the stream (which lets it by pdl_launch_dependents).
+template <typename... Params, typename... Args>
+int launch_after(void (*kernel)(Params...), dim3 grid, unsigned threads, cudaStream_t st, const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return QLORA_ERR_CUDA;
+  }
+  return launch_status();
+}
+
 // ------------------------------------------------------------------------------------------
 // kernel timing: CUDA events around each launch while a profile is open
 // ------------------------------------------------------------------------------------------
@@ -841,9 +862,8 @@ int fwd_core(const uint16_t* X, const uint16_t* Xl, int64_t t, const nf4_weight*
     ga.kb_per_split = (ga.num_kb + shares - 1) / shares;
     if ((rc = launch_nf4_gemm<false, kEpiPartial>(mA, mP, mA2, mB2, ga, t, o, st, prof::kGemmFwd, shares, part)))
       return rc;
-    nf4_gemm_join_kernel<<<static_cast<unsigned>((t * (o / 8) + 255) / 256), 256, 0, st>>>(part, shares, Y, t,
-                                                                                         ga.N, ga.epi);
-    return launch_status();
+    return launch_after(nf4_gemm_join_kernel, dim3(static_cast<unsigned>((t * (o / 8) + 255) / 256)), 256, st, part,
+                        shares, Y, t, ga.N, ga.epi);
   }
   return launch_nf4_gemm<false>(mA, mP, mA2, mB2, ga, t, o, st, prof::kGemmFwd);
 }

@@ -182,6 +182,7 @@ __global__ void __launch_bounds__(vg::kThreads, 1)
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(drained + 1);
   volatile uint32_t* abort_flag = tmem_holder + 1;
 
+  pdl_launch_dependents();
   if (kMode == kVocabProb && args.redo && *args.redo == 0u) return;   // (the whole grid alike)
   const int warp = uniform_warp(), lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_ctarank());   // 0: MMA issuer, 1: its peer
@@ -651,6 +652,7 @@ __global__ void __launch_bounds__(vn::kThreads, 1)
                         const __grid_constant__ CUtensorMap tmX, const VocabNarrowArgs args) {
   using namespace vn;
   extern __shared__ uint8_t smem_raw[];
+  pdl_launch_dependents();
   if (kMode == kVocabProb && args.redo && *args.redo == 0u) return;   // (the whole grid alike)
   const int warp = uniform_warp(), lane = threadIdx.x & 31;
   NarrowCta cta = narrow_setup(smem_raw, args.n16);
@@ -814,6 +816,7 @@ __global__ void __launch_bounds__(vn::kThreads, 1)
                              const VocabNarrowArgs args) {
   using namespace vn;
   extern __shared__ uint8_t smem_raw[];
+  pdl_launch_dependents();
   const int warp = uniform_warp(), lane = threadIdx.x & 31;
   NarrowCta cta = narrow_setup(smem_raw, args.n16);
   narrow_begin(cta);
@@ -909,6 +912,7 @@ __device__ __forceinline__ float2 join_stats(float2 p, float2 q) {
 template <int kWarps>
 __global__ void __launch_bounds__(256) vocab_rows_kernel(const VocabRowArgs a) {
   __shared__ float2 sh[8];
+  pdl_wait();
   const int row = blockIdx.x * (8 / kWarps) + (threadIdx.x >> 5) / kWarps, lane = threadIdx.x & 31;
   if (row >= a.t) return;   // (whole warps; with eight to a row no CTA is without one)
   float2 st = make_float2(-INFINITY, 0.f);
@@ -978,6 +982,7 @@ __global__ void __launch_bounds__(256)
 // dX tiles whose K was split: the partial tiles are added in order and rounded once.
 __global__ void __launch_bounds__(256)
     vocab_join_kernel(const float* part, uint16_t* dX, const VocabGemmArgs a) {
+  pdl_wait();
   const int tile = blockIdx.x, r = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   VocabGemmArgs b = a;
   b.splits = 1;
@@ -999,6 +1004,7 @@ __global__ void __launch_bounds__(256)
 // The same for few tokens: grid x a 128-column tile of h, grid y two tokens.
 __global__ void __launch_bounds__(256)
     vocab_narrow_join_kernel(const float* part, uint16_t* dX, const VocabNarrowArgs a, const VocabGemmArgs f, int ctas) {
+  pdl_wait();
   const int tile = blockIdx.x, col = threadIdx.x & 127, tok = blockIdx.y * 2 + (threadIdx.x >> 7);
   if (tok >= a.t || tile * vn::BM + col >= a.h) return;
   const int total = a.tiles * a.num_kb, base = total / ctas, extra = total - base * ctas;
