@@ -30,7 +30,7 @@ int launch_finish(const float* part_pre, const float* part_post, const float* pa
                           float* dw_post, float* dgate, int t, int h, int rows_per_gate, int parts, int units,
                           int grid_y, cudaStream_t st) {
   dim3 grid(static_cast<unsigned>((h + nr::kFinishCols - 1) / nr::kFinishCols), static_cast<unsigned>(grid_y));
-  return launch_after(norm_residual_finish_kernel, grid, nr::kFinishWarps * 32, st, part_pre, part_post, part_gate,
+  return launch_after(norm_residual_finish_kernel, grid, nr::kFinishWarps * 32, st, 0, part_pre, part_post, part_gate,
                       dw_pre, dw_post, dgate, t, h, rows_per_gate, parts, units);
 }
 
@@ -151,19 +151,21 @@ VocabGemmArgs plan_vocab_gemm(int64_t M, int64_t N, int64_t K, bool split, int p
 
 template <int kMode>
 int launch_vocab_gemm(const CUtensorMap& mA, const CUtensorMap& mB, const CUtensorMap& mOut,
-                      const CUtensorMap& mPart, const VocabGemmArgs& a, int pairs, cudaStream_t st) {
+                      const CUtensorMap& mPart, const VocabGemmArgs& a, int pairs, bool first, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(2 * std::min(pairs, a.items)), 1, 1);
   cfg.blockDim = dim3(vg::kThreads, 1, 1);
   cfg.dynamicSmemBytes = vg::smem_bytes();
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // (the kernels wait before they read)
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = first ? 1 : 2;   // a call's first kernel starts after all earlier work
   cudaError_t e;
   {
     prof::Scope ps(prof::kVocabGemm, st);
@@ -177,10 +179,13 @@ int launch_vocab_gemm(const CUtensorMap& mA, const CUtensorMap& mB, const CUtens
 }
 
 template <typename Kernel, typename... Maps>
-int launch_narrow(Kernel kernel, const VocabNarrowArgs& a, int ctas, cudaStream_t st, const Maps&... maps) {
+int launch_narrow(Kernel kernel, const VocabNarrowArgs& a, int ctas, bool first, cudaStream_t st, const Maps&... maps) {
   prof::Scope ps(prof::kVocabGemm, st);
-  kernel<<<static_cast<unsigned>(ctas), vn::kThreads, vn::smem_bytes(a.n16), st>>>(maps..., a);
-  return launch_status();
+  if (first) {   // a call's first kernel starts after all earlier work
+    kernel<<<static_cast<unsigned>(ctas), vn::kThreads, vn::smem_bytes(a.n16), st>>>(maps..., a);
+    return launch_status();
+  }
+  return launch_after(kernel, dim3(static_cast<unsigned>(ctas)), vn::kThreads, st, vn::smem_bytes(a.n16), maps..., a);
 }
 
 struct VocabCall {
@@ -239,7 +244,7 @@ int vocab_core(const VocabCall& c, void* workspace, cudaStream_t st) {
     prof::Scope ps(prof::kVocabRows, st);
     const bool few = n <= kFewRows;
     return launch_after(few ? vocab_rows_kernel<8> : vocab_rows_kernel<1>,
-                        dim3(static_cast<unsigned>(few ? n : (n + 7) / 8)), 256, st, r);
+                        dim3(static_cast<unsigned>(few ? n : (n + 7) / 8)), 256, st, 0, r);
   };
   if (p.narrow) {
     VocabNarrowArgs a{};
@@ -269,13 +274,13 @@ int vocab_core(const VocabCall& c, void* workspace, cudaStream_t st) {
     const int ctas = std::min(sm_count(dev), a.units);
     if (stats) {
       if (grad && (rc = run_targets(0, c.t))) return rc;
-      if ((rc = grad ? launch_narrow(vocab_narrow_kernel<kVocabScaled>, a, ctas, st, mW, mWu, mX)
-                     : launch_narrow(vocab_narrow_kernel<kVocabStats>, a, ctas, st, mW, mWu, mX)))
+      if ((rc = grad ? launch_narrow(vocab_narrow_kernel<kVocabScaled>, a, ctas, false, st, mW, mWu, mX)
+                     : launch_narrow(vocab_narrow_kernel<kVocabStats>, a, ctas, true, st, mW, mWu, mX)))
         return rc;
       if ((rc = run_rows(0, c.t))) return rc;
     }
     if (!grad) return QLORA_OK;
-    if ((rc = launch_narrow(vocab_narrow_kernel<kVocabProb>, a, ctas, st, mW, mWu, mX))) return rc;
+    if ((rc = launch_narrow(vocab_narrow_kernel<kVocabProb>, a, ctas, !stats, st, mW, mWu, mX))) return rc;
     CUtensorMap mWmn, mG;
     if (!map_bf16(&mWmn, c.W, c.h, c.v, 64, 64) ||
         !map_bf16(&mG, g, p.ldp, c.t, 64, static_cast<uint32_t>(a.n16)))
@@ -284,7 +289,7 @@ int vocab_core(const VocabCall& c, void* workspace, cudaStream_t st) {
     d.num_kb = (a.ldp + vn::KS * vn::BK - 1) / (vn::KS * vn::BK);
     d.tiles = static_cast<int>((c.h + vn::BM - 1) / vn::BM);
     const int gctas = static_cast<int>(std::min<int64_t>(sm_count(dev), static_cast<int64_t>(d.tiles) * d.num_kb));
-    if ((rc = launch_narrow(vocab_narrow_grad_kernel, d, gctas, st, mWmn, mG))) return rc;
+    if ((rc = launch_narrow(vocab_narrow_grad_kernel, d, gctas, false, st, mWmn, mG))) return rc;
     VocabGemmArgs f{};
     f.N = d.h;
     f.targets = c.targets;
@@ -296,8 +301,8 @@ int vocab_core(const VocabCall& c, void* workspace, cudaStream_t st) {
     }
     prof::Scope ps(prof::kVocabRows, st);
     return launch_after(vocab_narrow_join_kernel,
-                        dim3(static_cast<unsigned>(d.tiles), static_cast<unsigned>((c.t + 1) / 2)), 256, st, part, c.dX, d,
-                        f, gctas);
+                        dim3(static_cast<unsigned>(d.tiles), static_cast<unsigned>((c.t + 1) / 2)), 256, st, 0, part, c.dX,
+                        d, f, gctas);
   }
   CUtensorMap mWk, mWmn, mPart;
   if (!map_bf16(&mWk, c.W, c.h, c.v, 64, 128) || !map_bf16(&mWmn, c.W, c.h, c.v, 64, 64)) return QLORA_ERR_CUDA;
@@ -329,14 +334,14 @@ int vocab_core(const VocabCall& c, void* workspace, cudaStream_t st) {
         a.redo = redo;
         if ((rc = run_targets(i0, n))) return rc;
       }
-      rc = grad ? launch_vocab_gemm<kVocabScaled>(mX, mWk, mGs, mX, a, pairs, st)
-                : launch_vocab_gemm<kVocabStats>(mX, mWk, mX, mX, a, pairs, st);
+      rc = grad ? launch_vocab_gemm<kVocabScaled>(mX, mWk, mGs, mX, a, pairs, false, st)
+                : launch_vocab_gemm<kVocabStats>(mX, mWk, mX, mX, a, pairs, true, st);
       if (rc) return rc;
       if ((rc = run_rows(i0, n))) return rc;
     }
     if (!grad) continue;
     // g from lse: the backward alone, or again for a run whose scaled exponentials do not serve
-    if ((rc = launch_vocab_gemm<kVocabProb>(mX, mWk, mGs, mX, a, pairs, st))) return rc;
+    if ((rc = launch_vocab_gemm<kVocabProb>(mX, mWk, mGs, mX, a, pairs, !stats, st))) return rc;
     VocabGemmArgs d = plan_vocab_gemm(n, c.h, c.v, true, pairs);
     d.targets = a.targets;
     d.W = c.W;
@@ -345,10 +350,10 @@ int vocab_core(const VocabCall& c, void* workspace, cudaStream_t st) {
       d.redo = redo;
       d.factor = factor;
     }
-    if ((rc = launch_vocab_gemm<kVocabGrad>(mG, mWmn, mD, mPart, d, pairs, st))) return rc;
+    if ((rc = launch_vocab_gemm<kVocabGrad>(mG, mWmn, mD, mPart, d, pairs, false, st))) return rc;
     if (d.splits > 1) {
       const int tiles = d.m_tiles * d.n_tiles - d.whole;
-      if ((rc = launch_after(vocab_join_kernel, dim3(static_cast<unsigned>(tiles), vg::BM / 8), 256, st, part,
+      if ((rc = launch_after(vocab_join_kernel, dim3(static_cast<unsigned>(tiles), vg::BM / 8), 256, st, 0, part,
                              c.dX + i0 * c.h, d)))
         return rc;
     }

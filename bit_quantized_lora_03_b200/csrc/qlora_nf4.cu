@@ -274,13 +274,15 @@ int launch_status() {
   return e == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
 }
 
-// A kernel that begins with pdl_wait(), launched so that its start overlaps the end of the kernel before it on
+// A kernel that calls pdl_wait() before it reads or writes memory, launched so that its start overlaps the end of the kernel before it on
 // the stream (which lets it by pdl_launch_dependents).
 template <typename... Params, typename... Args>
-int launch_after(void (*kernel)(Params...), dim3 grid, unsigned threads, cudaStream_t st, const Args&... args) {
+int launch_after(void (*kernel)(Params...), dim3 grid, unsigned threads, cudaStream_t st, size_t smem,
+                 const Args&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -862,7 +864,7 @@ int fwd_core(const uint16_t* X, const uint16_t* Xl, int64_t t, const nf4_weight*
     ga.kb_per_split = (ga.num_kb + shares - 1) / shares;
     if ((rc = launch_nf4_gemm<false, kEpiPartial>(mA, mP, mA2, mB2, ga, t, o, st, prof::kGemmFwd, shares, part)))
       return rc;
-    return launch_after(nf4_gemm_join_kernel, dim3(static_cast<unsigned>((t * (o / 8) + 255) / 256)), 256, st, part,
+    return launch_after(nf4_gemm_join_kernel, dim3(static_cast<unsigned>((t * (o / 8) + 255) / 256)), 256, st, 0, part,
                         shares, Y, t, ga.N, ga.epi);
   }
   return launch_nf4_gemm<false>(mA, mP, mA2, mB2, ga, t, o, st, prof::kGemmFwd);

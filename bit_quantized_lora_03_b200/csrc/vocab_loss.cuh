@@ -183,7 +183,10 @@ __global__ void __launch_bounds__(vg::kThreads, 1)
   volatile uint32_t* abort_flag = tmem_holder + 1;
 
   pdl_launch_dependents();
-  if (kMode == kVocabProb && args.redo && *args.redo == 0u) return;   // (the whole grid alike)
+  if (kMode == kVocabProb) {
+    pdl_wait();
+    if (args.redo && *args.redo == 0u) return;   // (the whole grid alike)
+  }
   const int warp = uniform_warp(), lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_ctarank());   // 0: MMA issuer, 1: its peer
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
@@ -210,6 +213,7 @@ __global__ void __launch_bounds__(vg::kThreads, 1)
     tma_prefetch_desc(&tmB);
     tma_prefetch_desc(&tmOut);
   }
+  if (kMode != kVocabProb) pdl_wait();   // (before anything is read that a kernel of the same call wrote)
   tc_fence_before();
   __syncthreads();
   cluster_sync();   // both CTAs' barriers exist before any cross-CTA arrive
@@ -653,9 +657,13 @@ __global__ void __launch_bounds__(vn::kThreads, 1)
   using namespace vn;
   extern __shared__ uint8_t smem_raw[];
   pdl_launch_dependents();
-  if (kMode == kVocabProb && args.redo && *args.redo == 0u) return;   // (the whole grid alike)
+  if (kMode == kVocabProb) {
+    pdl_wait();
+    if (args.redo && *args.redo == 0u) return;   // (the whole grid alike)
+  }
   const int warp = uniform_warp(), lane = threadIdx.x & 31;
   NarrowCta cta = narrow_setup(smem_raw, args.n16);
+  if (kMode != kVocabProb) pdl_wait();
   // per token: what the epilogue needs of it (a word that is nobody's target: -1)
   float *t_ref = cta.token, *t_a = cta.token + kMaxTokens, *t_b = cta.token + 2 * kMaxTokens;
   int* t_word = reinterpret_cast<int*>(cta.token + 3 * kMaxTokens);
@@ -819,6 +827,7 @@ __global__ void __launch_bounds__(vn::kThreads, 1)
   pdl_launch_dependents();
   const int warp = uniform_warp(), lane = threadIdx.x & 31;
   NarrowCta cta = narrow_setup(smem_raw, args.n16);
+  pdl_wait();
   narrow_begin(cta);
   const int total = args.tiles * args.num_kb;
   const int x0 = unit_row(total, gridDim.x, blockIdx.x), x1 = unit_row(total, gridDim.x, blockIdx.x + 1);
@@ -912,6 +921,7 @@ __device__ __forceinline__ float2 join_stats(float2 p, float2 q) {
 template <int kWarps>
 __global__ void __launch_bounds__(256) vocab_rows_kernel(const VocabRowArgs a) {
   __shared__ float2 sh[8];
+  pdl_launch_dependents();
   pdl_wait();
   const int row = blockIdx.x * (8 / kWarps) + (threadIdx.x >> 5) / kWarps, lane = threadIdx.x & 31;
   if (row >= a.t) return;   // (whole warps; with eight to a row no CTA is without one)
@@ -953,6 +963,7 @@ __global__ void __launch_bounds__(256)
     vocab_target_kernel(const uint16_t* X, const uint16_t* W, const int64_t* targets, int64_t ignore, int t, int h,
                         int v, float* ref, unsigned* redo) {
   __shared__ float sh[8];
+  pdl_launch_dependents();
   const int row = blockIdx.x * (8 / kWarps) + (threadIdx.x >> 5) / kWarps, lane = threadIdx.x & 31;
   if (blockIdx.x == 0 && threadIdx.x == 0) *redo = 0u;
   if (row >= t) return;
