@@ -55,8 +55,7 @@ constexpr int STAGES = 3;
 constexpr int ATOM = 128 * BK * 2;           // this CTA's half of A, or of B, for one step
 constexpr int A_BYTES = KS * ATOM;
 constexpr int STAGE_BYTES = 2 * A_BYTES;
-constexpr int CHUNK = 4;                     // stages per accumulation of logits (K = 512); a tile's first
-                                             // takes twice that, while the tile before is finished
+constexpr int CHUNK = 4;                     // stages per accumulation of logits (K = 512)
 constexpr int PIECE = 128;                   // columns of a tile that one epilogue warp reduces
 constexpr int kEpiWarps = 8;                 // four for each half of a tile's columns
 constexpr int kTmaWarp = 8, kMmaWarp = 9;
@@ -167,7 +166,7 @@ __global__ void __launch_bounds__(vg::kThreads, 1)
                       const VocabGemmArgs args) {
   using namespace vg;
   auto chunk_end = [](const VocabItem& it, int kc) {
-    return kMode == kVocabGrad ? it.kb1 : min(it.kb1, kc + (kc == it.kb0 ? 2 * CHUNK : CHUNK));
+    return kMode == kVocabGrad ? it.kb1 : min(it.kb1, kc + CHUNK);
   };
   constexpr bool kBmn = kMode == kVocabGrad;   // W as the K-major operand (logits) or the MN-major one
   extern __shared__ uint8_t smem_raw[];
@@ -489,8 +488,7 @@ __global__ void __launch_bounds__(vg::kThreads, 1)
 // ------------------------------------------------------------------------------------------
 namespace vn {
 constexpr int kMaxTokens = 80;    // an epilogue thread's sums: one register per token
-// stages of the accumulation that starts at stage kc: K = 512 (1024 for a tile's first), as above
-__host__ __device__ constexpr int chunk(int kc) { return kc == 0 ? 8 : 4; }
+constexpr int CHUNK = 4;          // stages per accumulation of logits (K = 512), as above
 constexpr int BM = 128, BK = 64;
 constexpr int KS = 2;             // K-steps of 64 per stage: a stage's waits and copies cost some 700 cycles
                                   // whatever it holds, so that 16 KB of W each were not enough to keep up with HBM
@@ -716,8 +714,8 @@ __global__ void __launch_bounds__(vn::kThreads, 1)
     // accumulator rows are not read)
     bool ok = true;
     for (int u = u0; ok && u < u1; u += 4)
-      for (int kc = 0; ok && kc < args.num_kb; kc += chunk(kc), ++n)
-        ok = narrow_mma<false>(cta, args.n16, n & 1, n, min(chunk(kc), args.num_kb - kc), g);
+      for (int kc = 0; ok && kc < args.num_kb; kc += CHUNK, ++n)
+        ok = narrow_mma<false>(cta, args.n16, n & 1, n, min(CHUNK, args.num_kb - kc), g);
     narrow_drain_mma(cta, g);
   } else {
     int n = 0;
@@ -727,7 +725,7 @@ __global__ void __launch_bounds__(vn::kThreads, 1)
 #pragma unroll
       for (int j = 0; j < kMaxTokens; ++j) s[j] = 0.f;
 #pragma unroll 1
-      for (int kc = 0; kc < args.num_kb; kc += chunk(kc), ++n) {
+      for (int kc = 0; kc < args.num_kb; kc += CHUNK, ++n) {
         const int buf = n & 1;
         if (!mbar_wait_warp(&cta.acc_full[buf], (n >> 1) & 1, cta.abort_flag)) { ok = false; break; }
         tc_fence_after();
