@@ -549,6 +549,16 @@ constexpr int kPiecePairs = 256;   // input pairs staged at a time
 constexpr size_t smem_bytes(int t, int r) {
   return (static_cast<size_t>(2 * kThreads) * t + static_cast<size_t>(t) * r + static_cast<size_t>(kPiecePairs) * t) * 4;
 }
+// A thread takes column pair cp of k stride kg: kThreads / (r / 2) strides, which leaves the last
+// threads without one where that is not exact. A piece is a whole number of the loop's rounds of 4.
+__host__ __device__ constexpr int strides(int r) { return kThreads / (r / 2); }
+__host__ __device__ constexpr int piece_pairs(int r) { return kPiecePairs / (4 * strides(r)) * (4 * strides(r)); }
+constexpr bool pieces_fit() {
+  for (int r = 16; r <= gv::kMaxRank; r += 16)
+    if (piece_pairs(r) < 4 * strides(r) || piece_pairs(r) > kPiecePairs || strides(r) * r > 2 * kThreads) return false;
+  return true;
+}
+static_assert(pieces_fit(), "a piece is staged whole, and the strides' sums have their place");
 }  // namespace gd
 
 __global__ void __cluster_dims__(gd::kClusterCtas, 1, 1) __launch_bounds__(gd::kThreads)
@@ -573,15 +583,17 @@ __global__ void __cluster_dims__(gd::kClusterCtas, 1, 1) __launch_bounds__(gd::k
   }
 
   const int ncp = r / 2;                // column pairs
-  const int nkg = gd::kThreads / ncp;   // k strides
+  const int nkg = gd::strides(r);
   const int cp = tid % ncp, kg = tid / ncp;
+  const bool works = kg < nkg;          // the others stage and meet the barriers: the inputs of a stride of their
+                                        // own would lie behind the staged piece
   // this CTA's inputs: an even share of the 2-row pairs, walked in pieces whose activations (t x
   // piece) are staged in shared memory by coalesced loads: read one by one where they are used,
   // they cost a dependent load of 4 bytes for every token and pair
   const int64_t pairs = h / 2;
   const int64_t p0 = pairs * blockIdx.x / gd::kCtas, p1 = pairs * (blockIdx.x + 1) / gd::kCtas;
   uint32_t* xs = reinterpret_cast<uint32_t*>(dsm) + static_cast<size_t>(2 * gd::kThreads) * t + static_cast<size_t>(t) * r;
-  const int piece = gd::kPiecePairs / (4 * nkg) * (4 * nkg);   // whole rounds of the loop below
+  const int piece = gd::piece_pairs(r);
   float acc[16][2];
 #pragma unroll
   for (int n = 0; n < 16; ++n) acc[n][0] = acc[n][1] = 0.f;
@@ -594,7 +606,7 @@ __global__ void __cluster_dims__(gd::kClusterCtas, 1, 1) __launch_bounds__(gd::k
       for (int i = tid & 31; i < np; i += 32) xs[n * gd::kPiecePairs + i] = __ldg(xr + i);
     }
     __syncthreads();
-    for (int64_t pb = pp + kg; pb < pe; pb += 4 * nkg) {
+    for (int64_t pb = pp + kg; works && pb < pe; pb += 4 * nkg) {
       uint32_t la[4], lb[4];
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
@@ -606,7 +618,7 @@ __global__ void __cluster_dims__(gd::kClusterCtas, 1, 1) __launch_bounds__(gd::k
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const int64_t pr = pb + u * nkg;
-        if (pr >= p1) break;
+        if (pr >= pe) break;
         const float a0 = bf16_bits_to_float(la[u] & 0xffffu), a1 = bf16_bits_to_float(la[u] >> 16);
         const float b0 = bf16_bits_to_float(lb[u] & 0xffffu), b1 = bf16_bits_to_float(lb[u] >> 16);
         const uint32_t* xp = xs + static_cast<int>(pr - pp);
@@ -627,7 +639,7 @@ __global__ void __cluster_dims__(gd::kClusterCtas, 1, 1) __launch_bounds__(gd::k
   float* part = dsm + static_cast<size_t>(2 * gd::kThreads) * t;
 #pragma unroll
   for (int n = 0; n < 16; ++n)
-    if (n < t) {
+    if (works && n < t) {
       red[(kg * t + n) * r + 2 * cp] = acc[n][0];
       red[(kg * t + n) * r + 2 * cp + 1] = acc[n][1];
     }
