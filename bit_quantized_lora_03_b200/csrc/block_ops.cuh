@@ -298,6 +298,7 @@ int vocab_core(const VocabCall& c, void* workspace, cudaStream_t st) {
     if (stats) {
       f.redo = redo;
       f.factor = factor;
+      f.dloss = c.dloss;
     }
     prof::Scope ps(prof::kVocabRows, st);
     return launch_after(vocab_narrow_join_kernel,
@@ -349,6 +350,7 @@ int vocab_core(const VocabCall& c, void* workspace, cudaStream_t st) {
     if (stats) {
       d.redo = redo;
       d.factor = factor;
+      d.dloss = a.dloss;
     }
     if ((rc = launch_vocab_gemm<kVocabGrad>(mG, mWmn, mD, mPart, d, pairs, false, st))) return rc;
     if (d.splits > 1) {

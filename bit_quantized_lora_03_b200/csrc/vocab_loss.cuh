@@ -19,7 +19,8 @@
 //
 // Loss and gradient in one call form the logits once: exp(l - l[y]) needs nothing that is not known
 // when a piece's logits are, floating point keeps its relative precision whatever its scale, and the
-// row's factor dloss.exp(l[y] - lse) is applied to the finished dX. The logits l[y] come first, from a
+// row's factor exp(l[y] - lse) and then its dloss are applied to the finished dX (their product may be
+// too small for fp32 where the gradient is not). The logits l[y] come first, from a
 // kernel of their own (t dot products). The target's own term is left out of g and added in fp32 as
 // (a.p[y] - b).W[y] (with one call dloss.(exp(-loss) - 1).W[y]), so that a confident token's small
 // difference is not one of two rounded numbers and the largest term is not rounded to bf16. Only where
@@ -89,7 +90,7 @@ struct VocabGemmArgs {
   const float* dlse;     // or NULL
   unsigned* redo;        // kVocabScaled: raised by rows it cannot serve. kVocabProb: NULL, or the flag
                          // without which there is nothing to do. kVocabGrad: see row_factor
-  const float* factor;   // kVocabGrad: NULL, or the rows' factors
+  const float* factor;   // kVocabGrad: NULL, or the rows' factors, by which (and by dloss) g is still to be multiplied
   float* target_factor;  // kVocabProb writes, kVocabGrad reads: the factors of the targets' W
   const uint16_t* W;
 };
@@ -118,25 +119,30 @@ __device__ __forceinline__ VocabItem vocab_item(const VocabGemmArgs& a, int item
   return it;
 }
 
-// dX from the second product: a row's factor times it, plus its target's factor times W[target]. The row's
-// factor is 1 without factors, or after kVocabProb ran again (g is then complete).
+// dX from the second product: a row's factor and dloss times it, plus its target's factor times W[target].
+// Both are 1 without factors, or after kVocabProb ran again (g is then complete).
 struct RowFactor {
-  float f, ft;
+  float f, d, ft;
+  __device__ __forceinline__ float times(float v, float t) const {   // a row that counts for nothing: exactly zero
+    return f == 0.f ? 0.f : fmaf(v * f, d, ft * t);
+  }
   const uint16_t* w;   // the target's row of W, or NULL
   // eight columns from `col` on (col < the row's length, a multiple of 8)
   __device__ __forceinline__ void apply(float (&v)[8], int col) const {
     float t[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (w) unpack8(ldg_vec(w, col >> 3), t);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = f == 0.f ? 0.f : fmaf(v[e], f, ft * t[e]);   // not counted: exactly zero
+    for (int e = 0; e < 8; ++e) v[e] = times(v[e], t[e]);
   }
 };
 __device__ __forceinline__ RowFactor row_factor(const VocabGemmArgs& a, int row) {
   RowFactor r;
-  r.f = r.ft = 0.f;
+  r.f = r.d = r.ft = 0.f;
   r.w = nullptr;
   if (row >= 0) {
-    r.f = !a.factor || *a.redo != 0u ? 1.f : a.factor[row];
+    const bool whole = !a.factor || *a.redo != 0u;
+    r.f = whole ? 1.f : a.factor[row];
+    r.d = whole ? 1.f : a.dloss[row];
     r.ft = a.target_factor[row];
     if (r.ft != 0.f) r.w = a.W + a.targets[row] * a.N;   // (counted: inside the vocabulary)
   }
@@ -914,7 +920,7 @@ __device__ __forceinline__ float2 join_stats(float2 p, float2 q) {
   return make_float2(m, ps + qs);
 }
 
-// Loss, lse, and with dloss the factors of dX = factor.(g.W) + target_factor.W[y]. kWarps: a row's
+// Loss, lse, and with dloss the factors of dX = dloss.factor.(g.W) + target_factor.W[y]. kWarps: a row's
 // warps: one, or all eight of a CTA where there are few rows (its pieces then come in one go).
 template <int kWarps>
 __global__ void __launch_bounds__(256) vocab_rows_kernel(const VocabRowArgs a) {
@@ -950,7 +956,8 @@ __global__ void __launch_bounds__(256) vocab_rows_kernel(const VocabRowArgs a) {
   a.lse[row] = lse;
   if (a.dloss) {
     const float d = counted ? a.dloss[row] : 0.f;
-    a.factor[row] = counted ? d * expf(a.ref[row] - lse) : 0.f;
+    // not zero for a counted row: its loss is at most 60 + log v where factors are used
+    a.factor[row] = d != 0.f ? expf(a.ref[row] - lse) : 0.f;
     a.target_factor[row] = counted ? d * expm1f(-loss) : 0.f;  // dloss . (p[y] - 1)
   }
 }
@@ -1028,7 +1035,7 @@ __global__ void __launch_bounds__(256)
     s += __ldcg(part + (static_cast<int64_t>(i + tile) * a.n16 + tok) * vn::BM + col);
   const RowFactor rf = row_factor(f, tok);
   const int hc = tile * vn::BM + col;
-  s = rf.f == 0.f ? 0.f : fmaf(s, rf.f, rf.w ? rf.ft * bf16_bits_to_float(rf.w[hc]) : 0.f);
+  s = rf.times(s, rf.w ? bf16_bits_to_float(rf.w[hc]) : 0.f);
   dX[static_cast<int64_t>(tok) * a.h + hc] = __bfloat16_as_ushort(__float2bfloat16_rn(s));
 }
 
