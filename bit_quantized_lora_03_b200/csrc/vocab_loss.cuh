@@ -31,7 +31,8 @@
 // Logits are accumulated 512 inputs at a time in tensor memory and summed in the epilogue's registers.
 // The tensor core truncates its fp32 sum after every 16 inputs: over 4096 (8192) inputs a logit then
 // comes out 5e-6 (1.1e-5) of itself too small, which the loss, an fp32 value, would show; by pieces of
-// 512 it is 6e-7. g is rounded to bf16 anyway, and the second product accumulates as it comes.
+// 512 it is 6e-7. The second product, whose operand g and result are bf16, is accumulated 8192 words at a
+// time in the same way: 512 truncations of 2^-23 at most, 6e-5 of the terms' magnitudes.
 //
 // Bound: the tensor cores (2thv per product) for more than a few hundred tokens, reading W for few.
 // The design follows from the first: cta_group::2 (256 x 256 x 16 per instruction, each CTA loading
@@ -57,6 +58,7 @@ constexpr int ATOM = 128 * BK * 2;           // this CTA's half of A, or of B, f
 constexpr int A_BYTES = KS * ATOM;
 constexpr int STAGE_BYTES = 2 * A_BYTES;
 constexpr int CHUNK = 4;                     // stages per accumulation of logits (K = 512)
+constexpr int GRAD_CHUNK = 64;               // and of dX (K = 8192 words)
 constexpr int PIECE = 128;                   // columns of a tile that one epilogue warp reduces
 constexpr int kEpiWarps = 8;                 // four for each half of a tile's columns
 constexpr int kTmaWarp = 8, kMmaWarp = 9;
@@ -172,7 +174,7 @@ __global__ void __launch_bounds__(vg::kThreads, 1)
                       const VocabGemmArgs args) {
   using namespace vg;
   auto chunk_end = [](const VocabItem& it, int kc) {
-    return kMode == kVocabGrad ? it.kb1 : min(it.kb1, kc + CHUNK);
+    return min(it.kb1, kc + (kMode == kVocabGrad ? GRAD_CHUNK : CHUNK));
   };
   constexpr bool kBmn = kMode == kVocabGrad;   // W as the K-major operand (logits) or the MN-major one
   extern __shared__ uint8_t smem_raw[];
@@ -340,12 +342,6 @@ __global__ void __launch_bounds__(vg::kThreads, 1)
       return ready;
     };
     const uint32_t lane_addr = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(half * PIECE);
-    auto load64 = [&](int c, uint32_t (&v)[64]) {   // columns c .. c + 63 of this lane's row
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        tmem_ld_16(lane_addr + (n & 1) * BN + c + 16 * q, *reinterpret_cast<uint32_t(*)[16]>(&v[16 * q]));
-      tmem_ld_wait();
-    };
     auto release_acc = [&]() {   // the last read of this accumulation is behind
       tc_fence_before();
       __syncwarp();
@@ -358,40 +354,7 @@ __global__ void __launch_bounds__(vg::kThreads, 1)
       const int row0 = it.m0 + rank * 128 + quad * 32, row = row0 + lane;
       const int n0 = it.n0 + half * PIECE;   // this warp's first column
       const bool rok = row < args.M;
-      if (kMode == kVocabGrad) {
-        if (!wait_acc()) break;
-        const RowFactor rf = row_factor(args, it.part < 0 && rok ? row : -1);
-#pragma unroll 1
-        for (int c = 0; c < PIECE; c += 64) {
-          uint32_t v[64];
-          load64(c, v);
-          if (c + 64 == PIECE) release_acc();
-          uint4 q[8];
-          if (it.part < 0) {
-            if (n0 + c >= args.N) continue;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              float f[8];
-#pragma unroll
-              for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(v[8 * k + e]);
-              if (n0 + c + 8 * k < args.N) rf.apply(f, n0 + c + 8 * k);
-              q[k] = pack8(f);
-            }
-            store_tile(q, &tmOut, n0 + c, row0, row0 < args.M);
-          } else {
-#pragma unroll
-            for (int part = 0; part < 2; ++part) {
-#pragma unroll
-              for (int k = 0; k < 8; ++k)
-                q[k] = make_uint4(v[32 * part + 4 * k], v[32 * part + 4 * k + 1], v[32 * part + 4 * k + 2],
-                                  v[32 * part + 4 * k + 3]);
-              store_tile(q, &tmPart, half * PIECE + c + 32 * part, it.part * BM + rank * 128 + quad * 32, true);
-            }
-          }
-        }
-        continue;
-      }
-      // ---- logits ----------------------------------------------------------------------------------
+      // the tile's sums over its accumulations
       float s[PIECE];
 #pragma unroll
       for (int e = 0; e < PIECE; ++e) s[e] = 0.f;
@@ -409,6 +372,35 @@ __global__ void __launch_bounds__(vg::kThreads, 1)
         release_acc();
       }
       if (!ok) break;
+      if (kMode == kVocabGrad) {
+        const RowFactor rf = row_factor(args, it.part < 0 && rok ? row : -1);
+#pragma unroll
+        for (int c = 0; c < PIECE; c += 64) {
+          uint4 q[8];
+          if (it.part < 0) {
+            if (n0 + c >= args.N) break;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              float (&f)[8] = *reinterpret_cast<float(*)[8]>(&s[c + 8 * k]);
+              if (n0 + c + 8 * k < args.N) rf.apply(f, n0 + c + 8 * k);
+              q[k] = pack8(f);
+            }
+            store_tile(q, &tmOut, n0 + c, row0, row0 < args.M);
+          } else {
+#pragma unroll
+            for (int part = 0; part < 2; ++part) {
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const float* f = &s[c + 32 * part + 4 * k];
+                q[k] = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+              }
+              store_tile(q, &tmPart, half * PIECE + c + 32 * part, it.part * BM + rank * 128 + quad * 32, true);
+            }
+          }
+        }
+        continue;
+      }
+      // ---- logits ----------------------------------------------------------------------------------
       const int vcols = args.N - n0;   // columns behind the vocabulary read as zero products and count as -inf
       if (vcols < PIECE) {
 #pragma unroll
@@ -495,6 +487,7 @@ __global__ void __launch_bounds__(vg::kThreads, 1)
 namespace vn {
 constexpr int kMaxTokens = 80;    // an epilogue thread's sums: one register per token
 constexpr int CHUNK = 4;          // stages per accumulation of logits (K = 512), as above
+constexpr int GRAD_CHUNK = 64;    // and of dX (K = 8192 words)
 constexpr int BM = 128, BK = 64;
 constexpr int KS = 2;             // K-steps of 64 per stage: a stage's waits and copies cost some 700 cycles
                                   // whatever it holds, so that 16 KB of W each were not enough to keep up with HBM
@@ -836,6 +829,7 @@ __global__ void __launch_bounds__(vn::kThreads, 1)
   const int total = args.tiles * args.num_kb;
   const int x0 = unit_row(total, gridDim.x, blockIdx.x), x1 = unit_row(total, gridDim.x, blockIdx.x + 1);
   auto share_end = [&](int x) { return min(x1, (x / args.num_kb + 1) * args.num_kb); };
+  auto chunk_end = [&](int x) { return min(share_end(x), x + GRAD_CHUNK); };   // of one accumulation
 
   if (warp == kTmaWarp) {
     RingPos g;
@@ -864,28 +858,40 @@ __global__ void __launch_bounds__(vn::kThreads, 1)
   } else if (warp == kMmaWarp) {
     RingPos g;
     int n = 0;
-    for (int x = x0; x < x1; x = share_end(x), ++n)
-      if (!narrow_mma<true>(cta, args.n16, n & 1, n, share_end(x) - x, g)) break;
+    for (int x = x0; x < x1; x = chunk_end(x), ++n)
+      if (!narrow_mma<true>(cta, args.n16, n & 1, n, chunk_end(x) - x, g)) break;
     narrow_drain_mma(cta, g);
   } else {
     int n = 0;
-    for (int x = x0; x < x1; x = share_end(x), ++n) {
-      const int buf = n & 1;
-      if (!mbar_wait_warp(&cta.acc_full[buf], (n >> 1) & 1, cta.abort_flag)) break;
-      tc_fence_after();
-      const uint32_t taddr = cta.tmem + (static_cast<uint32_t>(warp * 32) << 16) + buf * (cta.tmem_cols / 2);
-      float* dst = args.part + static_cast<int64_t>(blockIdx.x + x / args.num_kb) * args.n16 * BM + warp * 32 + lane;
-      for (int c = 0; c < args.n16; c += 16) {
-        uint32_t v[16];
-        tmem_ld_16(taddr + c, v);
-        tmem_ld_wait();
+    bool ok = true;
+    for (int x = x0; ok && x < x1; x = share_end(x)) {
+      float s[kMaxTokens];
 #pragma unroll
-        for (int j = 0; j < 16; ++j)
-          if (c + j < args.t) dst[static_cast<int64_t>(c + j) * BM] = __uint_as_float(v[j]);
+      for (int j = 0; j < kMaxTokens; ++j) s[j] = 0.f;
+#pragma unroll 1
+      for (int k = x; k < share_end(x); k = chunk_end(k), ++n) {
+        const int buf = n & 1;
+        if (!mbar_wait_warp(&cta.acc_full[buf], (n >> 1) & 1, cta.abort_flag)) { ok = false; break; }
+        tc_fence_after();
+        const uint32_t taddr = cta.tmem + (static_cast<uint32_t>(warp * 32) << 16) + buf * (cta.tmem_cols / 2);
+#pragma unroll
+        for (int c = 0; c < kMaxTokens; c += 16) {
+          if (c >= args.n16) break;
+          uint32_t v[16];
+          tmem_ld_16(taddr + c, v);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 16; ++j) s[c + j] += __uint_as_float(v[j]);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&cta.acc_empty[buf]);
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&cta.acc_empty[buf]);
+      if (!ok) break;
+      float* dst = args.part + static_cast<int64_t>(blockIdx.x + x / args.num_kb) * args.n16 * BM + warp * 32 + lane;
+#pragma unroll
+      for (int j = 0; j < kMaxTokens; ++j)
+        if (j < args.t) dst[static_cast<int64_t>(j) * BM] = s[j];
     }
   }
   narrow_end(cta);

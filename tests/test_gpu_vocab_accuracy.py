@@ -49,3 +49,36 @@ def test_small_upstream_gradients_of_large_losses(t, dloss):
     e = dloss * (p + hot) @ W.double().abs() * (U16 + (h + 8) * 2 * U32 * 160)
     assert_within(dX, want, U16 * (want.abs() + e) + e, "dX")
     assert B.last_status() == 0
+
+
+@pytest.mark.parametrize("t,h,v", [(300, 64, 1 << 22), (20, 2048, 1 << 21), (100, 4096, 1 << 20)])
+def test_gradient_over_a_long_vocabulary_is_summed_in_pieces(t, h, v):
+    """X = 0, so that p is 2^-k for every word, and the target's row of W is the mean of all rows in bf16:
+    dX is what is left of the mean, and shows the sum's own error. The tensor core truncates its fp32 sum
+    after every 16 words; at most 8192 words are summed there, 512 truncations of 2^-23 of the magnitudes
+    and 16 more for the products of one step. The pieces' sums, v / 8192 of them, and up to 16 shares of a
+    split sum are added in fp32, each to 2^-24 of the whole."""
+    g = torch.Generator("cuda")
+    g.manual_seed(v)
+    W = torch.empty(v, h, dtype=torch.bfloat16, device="cuda")
+    total = torch.zeros(h, dtype=torch.float64, device="cuda")
+    step = (1 << 26) // h
+    for i in range(0, v, step):
+        W[i:i + step] = torch.rand(step, h, generator=g, device="cuda").bfloat16()
+        total += W[i:i + step].double().sum(0)
+    y = torch.full((t,), v // 3, device="cuda")
+    total -= W[v // 3].double()
+    W[v // 3] = (total / (v - 1)).bfloat16()
+    total += W[v // 3].double()
+    mean = total / v
+    want = (mean - W[v // 3].double()).expand(t, h)
+    X = torch.zeros(t, h, dtype=torch.bfloat16, device="cuda")
+    d = torch.ones(t, device="cuda")
+    loss, lse, dX = B.qlora_vocab_loss_fwd_bwd(X, W, y, d)
+    back = B.qlora_vocab_loss_bwd(X, W, y, lse, d)
+    # lse, and with it the row's factor, is off by a few units of fp32 and the 600 roundings of a row's sum
+    # of exponentials (p from lse, 2^-k but for that, is 2^-k again in bf16)
+    e = mean * ((512 + 16) * 2 + v / 8192 + 16 + 600 + 64) * U32
+    for got, name in ((dX, "dX"), (back, "dX from lse")):
+        assert_within(got, want, U16 * (want.abs() + e) + e, name)
+    assert B.last_status() == 0
