@@ -829,7 +829,6 @@ __global__ void __launch_bounds__(vn::kThreads, 1)
   const int total = args.tiles * args.num_kb;
   const int x0 = unit_row(total, gridDim.x, blockIdx.x), x1 = unit_row(total, gridDim.x, blockIdx.x + 1);
   auto share_end = [&](int x) { return min(x1, (x / args.num_kb + 1) * args.num_kb); };
-  auto chunk_end = [&](int x) { return min(share_end(x), x + GRAD_CHUNK); };   // of one accumulation
 
   if (warp == kTmaWarp) {
     RingPos g;
@@ -858,40 +857,41 @@ __global__ void __launch_bounds__(vn::kThreads, 1)
   } else if (warp == kMmaWarp) {
     RingPos g;
     int n = 0;
-    for (int x = x0; x < x1; x = chunk_end(x), ++n)
-      if (!narrow_mma<true>(cta, args.n16, n & 1, n, chunk_end(x) - x, g)) break;
+    bool ok = true;
+    for (int x = x0; ok && x < x1;)
+      for (const int end = share_end(x); ok && x < end; x = min(end, x + GRAD_CHUNK), ++n)   // one accumulation
+        ok = narrow_mma<true>(cta, args.n16, n & 1, n, min(end - x, GRAD_CHUNK), g);
     narrow_drain_mma(cta, g);
   } else {
     int n = 0;
     bool ok = true;
-    for (int x = x0; ok && x < x1; x = share_end(x)) {
-      float s[kMaxTokens];
-#pragma unroll
-      for (int j = 0; j < kMaxTokens; ++j) s[j] = 0.f;
-#pragma unroll 1
-      for (int k = x; k < share_end(x); k = chunk_end(k), ++n) {
+    for (int x = x0, end; ok && x < x1; x = end) {
+      end = share_end(x);
+      float* dst = args.part + static_cast<int64_t>(blockIdx.x + x / args.num_kb) * args.n16 * BM + warp * 32 + lane;
+      for (int k = x; k < end; k += GRAD_CHUNK, ++n) {
         const int buf = n & 1;
         if (!mbar_wait_warp(&cta.acc_full[buf], (n >> 1) & 1, cta.abort_flag)) { ok = false; break; }
         tc_fence_after();
         const uint32_t taddr = cta.tmem + (static_cast<uint32_t>(warp * 32) << 16) + buf * (cta.tmem_cols / 2);
-#pragma unroll
-        for (int c = 0; c < kMaxTokens; c += 16) {
-          if (c >= args.n16) break;
+        // a share's later accumulations are added to what this thread stored of the ones before
+        for (int c = 0; c < args.n16; c += 16) {
           uint32_t v[16];
           tmem_ld_16(taddr + c, v);
           tmem_ld_wait();
+          float* d = dst + static_cast<int64_t>(c) * BM;
+          if (k > x) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j) s[c + j] += __uint_as_float(v[j]);
+            for (int j = 0; j < 16; ++j)
+              if (c + j < args.t) v[j] = __float_as_uint(d[j * BM] + __uint_as_float(v[j]));
+          }
+#pragma unroll
+          for (int j = 0; j < 16; ++j)
+            if (c + j < args.t) d[j * BM] = __uint_as_float(v[j]);
         }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&cta.acc_empty[buf]);
       }
-      if (!ok) break;
-      float* dst = args.part + static_cast<int64_t>(blockIdx.x + x / args.num_kb) * args.n16 * BM + warp * 32 + lane;
-#pragma unroll
-      for (int j = 0; j < kMaxTokens; ++j)
-        if (j < args.t) dst[static_cast<int64_t>(j) * BM] = s[j];
     }
   }
   narrow_end(cta);
@@ -961,9 +961,9 @@ __global__ void __launch_bounds__(256) vocab_rows_kernel(const VocabRowArgs a) {
   a.loss[row] = loss;
   a.lse[row] = lse;
   if (a.dloss) {
-    const float d = counted ? a.dloss[row] : 0.f;
+    const float d = counted ? a.dloss[row] : 0.f, ref = counted ? a.ref[row] : 0.f;
     // not zero for a counted row: its loss is at most 60 + log v where factors are used
-    a.factor[row] = d != 0.f ? expf(a.ref[row] - lse) : 0.f;
+    a.factor[row] = d != 0.f ? expf(ref - lse) : 0.f;
     a.target_factor[row] = counted ? d * expm1f(-loss) : 0.f;  // dloss . (p[y] - 1)
   }
 }
