@@ -156,6 +156,18 @@ def _ptr(t: torch.Tensor | None) -> int | None:
     return None if t is None else t.data_ptr()
 
 
+def _used_on(stream, *tensors) -> None:
+    """Notes that work on `stream` (None: the current one) uses the tensors, which the caller may free as
+    soon as the call returns: their memory is then not given out again before that work is done."""
+    if stream is None:
+        return
+    for t in tensors:
+        if isinstance(t, PackedNF4):
+            _used_on(stream, t.codes, t.absmax_q8, t.absmax_s2)
+        elif t is not None:
+            t.record_stream(stream)
+
+
 CODEBOOK_NF4, CODEBOOK_FP4, CODEBOOK_INT4 = 0, 1, 2
 SCALES_U8, SCALES_S8, SCALES_E4M3 = 0, 1, 2
 
@@ -218,6 +230,7 @@ def nf4_quantize(Wt: torch.Tensor, out: PackedNF4 | None = None, stream=None,
     else:
         _check(lib().qlora_quantize_codebook(Wt.data_ptr(), ctypes.byref(d), int(codebook_id),
                                              _stream(stream)), "qlora_quantize_codebook")
+    _used_on(stream, Wt, p)
     return p
 
 
@@ -240,6 +253,7 @@ def nf4_dequantize(p: PackedNF4, out: torch.Tensor | None = None, stream=None,
     else:
         _check(lib().qlora_dequantize_codebook(ctypes.byref(d), int(codebook_id), out.data_ptr(),
                                                _stream(stream)), "qlora_dequantize_codebook")
+    _used_on(stream, p, out)
     return out
 
 
@@ -287,6 +301,7 @@ def qlora_linear_fwd(X: torch.Tensor, p: PackedNF4, L1: torch.Tensor, L2: torch.
                                 float(s), Y.data_ptr(), _ptr(sT), ws.data_ptr(), ws.numel(),
                                 _stream(stream))
     _check(rc, "qlora_linear_fwd")
+    _used_on(stream, X, p, L1, L2, Y, sT, ws)
     return Y, sT
 
 
@@ -317,6 +332,7 @@ def qlora_linear_bwd(dY: torch.Tensor, X: torch.Tensor, p: PackedNF4, L1: torch.
                                 dL1.data_ptr(), dL2.data_ptr(), ws.data_ptr(), ws.numel(),
                                 _stream(stream))
     _check(rc, "qlora_linear_bwd")
+    _used_on(stream, dY, X, p, L1, L2, sT, dX, dL1, dL2, ws)
     return dX, dL1, dL2
 
 
@@ -337,6 +353,7 @@ def qlora_dropout_apply(X: torch.Tensor, dropout_p: float, seed: int,
     pf, sd = _dropout_args(dropout_p, seed)
     _check(lib().qlora_dropout_apply(X.data_ptr(), t, h, pf, sd, out.data_ptr(), _stream(stream)),
            "qlora_dropout_apply")
+    _used_on(stream, X, out)
     return out
 
 
@@ -375,6 +392,7 @@ def qlora_linear_fwd_dropout(X: torch.Tensor, p: PackedNF4, L1: torch.Tensor, L2
                                         L2.data_ptr(), r, float(s), pf, sd, Y.data_ptr(), _ptr(sT),
                                         _ptr(mask), ws.data_ptr(), ws.numel(), _stream(stream))
     _check(rc, "qlora_linear_fwd_dropout")
+    _used_on(stream, X, p, L1, L2, Y, sT, mask, ws)
     return Y, sT, mask
 
 
@@ -409,6 +427,7 @@ def qlora_linear_bwd_dropout(dY: torch.Tensor, X: torch.Tensor, p: PackedNF4, L1
                                         _ptr(mask), dX.data_ptr(), dL1.data_ptr(), dL2.data_ptr(),
                                         ws.data_ptr(), ws.numel(), _stream(stream))
     _check(rc, "qlora_linear_bwd_dropout")
+    _used_on(stream, dY, X, p, L1, L2, sT, mask, dX, dL1, dL2, ws)
     return dX, dL1, dL2
 
 
@@ -416,7 +435,7 @@ def qlora_linear_bwd_dropout(dY: torch.Tensor, X: torch.Tensor, p: PackedNF4, L1
 # The operators around the linear. They run on the device of their tensors (all on one) and on the
 # current stream there, or on `stream`; what they allocate (outputs, workspace) is allocated on
 # that stream, one workspace per call, so that calls on two streams, and graphs captured from them,
-# share none.
+# share none. Their inputs may be freed as soon as they return.
 # ------------------------------------------------------------------------------------------
 _NO_GUARD = contextlib.nullcontext()
 
@@ -515,6 +534,7 @@ def qlora_linear_fwd_epilogue(X: torch.Tensor, p: PackedNF4, L1: torch.Tensor, L
             ins[0], t, ctypes.byref(d), ins[1], ins[2], r, float(s), ins[3], _act_id(act), ins[4],
             Y.data_ptr(), _ptr(Z), _ptr(sT), ws.data_ptr(), ws.numel(), _current(dev)),
             "qlora_linear_fwd_epilogue")
+    _used_on(stream, X, p, L1, L2, bias, residual, Y, Z, sT, ws)
     return Y, Z, sT
 
 
@@ -534,6 +554,7 @@ def qlora_epilogue_bwd(dY: torch.Tensor, Z: torch.Tensor | None, act="none",
         _check(lib().qlora_epilogue_bwd(a, z, t, o, _act_id(act), _ptr(dZ), _ptr(dbias), _ptr(ws),
                                         0 if ws is None else ws.numel(), _current(dev)),
                "qlora_epilogue_bwd")
+    _used_on(stream, dY, Z, dZ, dbias, ws)
     return dZ, dbias
 
 
@@ -566,6 +587,7 @@ def qlora_norm_residual_fwd(x: torch.Tensor, y: torch.Tensor | None = None,
         _check(lib().qlora_norm_residual_fwd(xp, yp, t, h, wo, gp, rows, float(scale), wi, float(eps),
                                              x_out.data_ptr(), _ptr(n), _ptr(ro), _ptr(ri), _current(dev)),
                "qlora_norm_residual_fwd")
+    _used_on(stream, x, y, w_post, gate, w_pre, x_out, n)
     return x_out, n, ro, ri
 
 
@@ -604,6 +626,7 @@ def qlora_norm_residual_bwd(dx_out: torch.Tensor | None, dn: torch.Tensor | None
                "qlora_norm_residual_bwd")
         if dn is None and w_pre is not None:
             dwi = torch.zeros(h, dtype=f32, device=dev)
+    _used_on(stream, dx_out, dn, x_out, y, rstd_post, rstd_pre, w_post, gate, w_pre, ws)
     return dx, dy, dwo, dg, dwi
 
 
@@ -627,6 +650,7 @@ def qlora_vocab_loss_fwd(X: torch.Tensor, W: torch.Tensor, targets: torch.Tensor
         ws = _scratch(dev, ws, int(lib().qlora_vocab_loss_fwd_workspace_bytes(t, h, v)))
         _check(lib().qlora_vocab_loss_fwd(*args, int(ignore_index), loss.data_ptr(), lse.data_ptr(),
                                           ws.data_ptr(), ws.numel(), _current(dev)), "qlora_vocab_loss_fwd")
+    _used_on(stream, X, W, targets, loss, lse, ws)
     return loss, lse
 
 
@@ -643,6 +667,7 @@ def qlora_vocab_loss_bwd(X: torch.Tensor, W: torch.Tensor, targets: torch.Tensor
         ws = _scratch(dev, ws, int(lib().qlora_vocab_loss_bwd_workspace_bytes(t, h, v)))
         _check(lib().qlora_vocab_loss_bwd(*args, int(ignore_index), *grads, dX.data_ptr(), ws.data_ptr(),
                                           ws.numel(), _current(dev)), "qlora_vocab_loss_bwd")
+    _used_on(stream, X, W, targets, lse, dloss, dlse, dX, ws)
     return dX
 
 
@@ -663,6 +688,7 @@ def qlora_vocab_loss_fwd_bwd(X: torch.Tensor, W: torch.Tensor, targets: torch.Te
         _check(lib().qlora_vocab_loss_fwd_bwd(*args, int(ignore_index), d, loss.data_ptr(), lse.data_ptr(),
                                               dX.data_ptr(), ws.data_ptr(), ws.numel(), _current(dev)),
                "qlora_vocab_loss_fwd_bwd")
+    _used_on(stream, X, W, targets, dloss, loss, lse, dX, ws)
     return loss, lse, dX
 
 
@@ -708,6 +734,7 @@ def merge_adapters(p: PackedNF4, L1: torch.Tensor, L2: torch.Tensor, s: float,
     _check(lib().qlora_merge_adapters(ctypes.byref(d), L1.data_ptr(), L2.data_ptr(), r,
                                       float(s), out.data_ptr(), _stream(stream)),
            "qlora_merge_adapters")
+    _used_on(stream, p, L1, L2, out)
     return out
 
 
@@ -736,6 +763,7 @@ def adamw_step(p: torch.Tensor, g: torch.Tensor, m: torch.Tensor, v: torch.Tenso
     adamw_step_ptr(p.data_ptr(), p16.data_ptr() if p16 is not None else 0, g.data_ptr(),
                    m.data_ptr(), v.data_ptr(), p.numel(), lr, beta1, beta2, eps, weight_decay,
                    step, 0, stream)
+    _used_on(stream, p, g, m, v, p16)
 
 
 ADAMW_MAX_TENSORS = 64
@@ -778,6 +806,7 @@ def adamw_step_multi(params, grads, ms, vs, step: int, lr: float = 1e-4, beta1: 
                          [m.data_ptr() for m in ms], [v.data_ptr() for v in vs],
                          [p.numel() for p in params], lr, beta1, beta2, eps, weight_decay, step, 0,
                          stream)
+    _used_on(stream, *params, *grads, *ms, *vs, *(params_bf16 or ()))
 
 
 def selftest_wait_timeout(limit_ns: int, stream=None) -> None:
