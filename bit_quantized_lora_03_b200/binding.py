@@ -101,7 +101,7 @@ SIGNATURES = {
     "qlora_vocab_loss_bwd_workspace_bytes": (ctypes.c_size_t, [_I64, _I64, _I64]),
     "qlora_vocab_loss_fwd_bwd_workspace_bytes": (ctypes.c_size_t, [_I64, _I64, _I64]),
 }
-KERNEL_KINDS = 12
+KERNEL_KINDS = 13
 
 
 class NF4WeightDesc(ctypes.Structure):

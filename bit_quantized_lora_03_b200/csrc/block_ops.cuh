@@ -26,12 +26,12 @@ int epilogue_runs(int64_t t, int64_t o, int sms, int ctas) {
   return static_cast<int>(runs);
 }
 
-int launch_finish(const float* part_pre, const float* part_post, const float* part_gate, float* dw_pre,
-                          float* dw_post, float* dgate, int t, int h, int rows_per_gate, int parts, int units,
-                          int grid_y, cudaStream_t st) {
+int launch_finish(int prof_kind, const float* part_pre, const float* part_post, const float* part_gate, float* dw_pre,
+                  float* dw_post, float* dgate, int t, int h, int rows_per_gate, int parts, int units, int grid_y,
+                  cudaStream_t st) {
   dim3 grid(static_cast<unsigned>((h + nr::kFinishCols - 1) / nr::kFinishCols), static_cast<unsigned>(grid_y));
-  return launch_after(norm_residual_finish_kernel, grid, nr::kFinishWarps * 32, st, 0, part_pre, part_post, part_gate,
-                      dw_pre, dw_post, dgate, t, h, rows_per_gate, parts, units);
+  return launch_after(prof_kind, norm_residual_finish_kernel, grid, nr::kFinishWarps * 32, st, 0, part_pre, part_post,
+                      part_gate, dw_pre, dw_post, dgate, t, h, rows_per_gate, parts, units);
 }
 
 // ------------------------------------------------------------------------------------------
@@ -180,12 +180,13 @@ int launch_vocab_gemm(const CUtensorMap& mA, const CUtensorMap& mB, const CUtens
 
 template <typename Kernel, typename... Maps>
 int launch_narrow(Kernel kernel, const VocabNarrowArgs& a, int ctas, bool first, cudaStream_t st, const Maps&... maps) {
-  prof::Scope ps(prof::kVocabGemm, st);
   if (first) {   // a call's first kernel starts after all earlier work
+    prof::Scope ps(prof::kVocabGemm, st);
     kernel<<<static_cast<unsigned>(ctas), vn::kThreads, vn::smem_bytes(a.n16), st>>>(maps..., a);
     return launch_status();
   }
-  return launch_after(kernel, dim3(static_cast<unsigned>(ctas)), vn::kThreads, st, vn::smem_bytes(a.n16), maps..., a);
+  return launch_after(prof::kVocabGemm, kernel, dim3(static_cast<unsigned>(ctas)), vn::kThreads, st,
+                      vn::smem_bytes(a.n16), maps..., a);
 }
 
 struct VocabCall {
@@ -241,9 +242,8 @@ int vocab_core(const VocabCall& c, void* workspace, cudaStream_t st) {
       r.factor = factor;
       r.target_factor = target_factor;
     }
-    prof::Scope ps(prof::kVocabRows, st);
     const bool few = n <= kFewRows;
-    return launch_after(few ? vocab_rows_kernel<8> : vocab_rows_kernel<1>,
+    return launch_after(prof::kVocabRows, few ? vocab_rows_kernel<8> : vocab_rows_kernel<1>,
                         dim3(static_cast<unsigned>(few ? n : (n + 7) / 8)), 256, st, 0, r);
   };
   if (p.narrow) {
@@ -300,8 +300,7 @@ int vocab_core(const VocabCall& c, void* workspace, cudaStream_t st) {
       f.factor = factor;
       f.dloss = c.dloss;
     }
-    prof::Scope ps(prof::kVocabRows, st);
-    return launch_after(vocab_narrow_join_kernel,
+    return launch_after(prof::kVocabRows, vocab_narrow_join_kernel,
                         dim3(static_cast<unsigned>(d.tiles), static_cast<unsigned>((c.t + 1) / 2)), 256, st, 0, part, c.dX,
                         d, f, gctas);
   }
@@ -355,8 +354,8 @@ int vocab_core(const VocabCall& c, void* workspace, cudaStream_t st) {
     if ((rc = launch_vocab_gemm<kVocabGrad>(mG, mWmn, mD, mPart, d, pairs, false, st))) return rc;
     if (d.splits > 1) {
       const int tiles = d.m_tiles * d.n_tiles - d.whole;
-      if ((rc = launch_after(vocab_join_kernel, dim3(static_cast<unsigned>(tiles), vg::BM / 8), 256, st, 0, part,
-                             c.dX + i0 * c.h, d)))
+      if ((rc = launch_after(prof::kVocabRows, vocab_join_kernel, dim3(static_cast<unsigned>(tiles), vg::BM / 8), 256, st, 0,
+                             part, c.dX + i0 * c.h, d)))
         return rc;
     }
   }
@@ -443,7 +442,7 @@ int qlora_epilogue_bwd(const uint16_t* dY, const uint16_t* Z, int64_t t, int64_t
   }
   if ((rc = launch_status())) return rc;
   if (!dbias || runs == 1) return QLORA_OK;
-  return launch_finish(a.part, nullptr, nullptr, dbias, nullptr, nullptr, static_cast<int>(t), a.o, 1, runs, 0, 1, st);
+  return launch_finish(prof::kEpilogueBwd, a.part, nullptr, nullptr, dbias, nullptr, nullptr, static_cast<int>(t), a.o, 1, runs, 0, 1, st);
 }
 
 int qlora_norm_residual_fwd(const uint16_t* x, const uint16_t* y, int64_t t, int64_t h, const uint16_t* w_post,
@@ -586,8 +585,8 @@ int qlora_norm_residual_bwd(const uint16_t* dx_out, const uint16_t* dn, const ui
   float* pre = pl.ctas > 1 ? dw_pre : nullptr;
   float* post = pl.ctas > 1 ? dw_post : nullptr;
   if (!pre && !post && !gate_blocks) return QLORA_OK;
-  return launch_finish(a.part_pre, a.part_post, a.part_gate, pre, post, dgate, a.t, a.h, a.rows_per_gate, pl.ctas,
-                       pl.units, 2 + gate_blocks, st);
+  return launch_finish(prof::kNorm, a.part_pre, a.part_post, a.part_gate, pre, post, dgate, a.t, a.h, a.rows_per_gate,
+                       pl.ctas, pl.units, 2 + gate_blocks, st);
 }
 
 size_t qlora_vocab_loss_fwd_workspace_bytes(int64_t t, int64_t h, int64_t v) {

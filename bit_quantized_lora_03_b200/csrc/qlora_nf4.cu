@@ -274,42 +274,20 @@ int launch_status() {
   return e == cudaSuccess ? QLORA_OK : QLORA_ERR_CUDA;
 }
 
-// A kernel that calls pdl_wait() before it reads or writes memory, launched so that its start overlaps the end of the kernel before it on
-// the stream (which lets it by pdl_launch_dependents).
-template <typename... Params, typename... Args>
-int launch_after(void (*kernel)(Params...), dim3 grid, unsigned threads, cudaStream_t st, size_t smem,
-                 const Args&... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads, 1, 1);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
-  if (e != cudaSuccess) {
-    cudaGetLastError();
-    return QLORA_ERR_CUDA;
-  }
-  return launch_status();
-}
-
 // ------------------------------------------------------------------------------------------
 // kernel timing: CUDA events around each launch while a profile is open
 // ------------------------------------------------------------------------------------------
 namespace prof {
 enum Kind {
   kQuant = 0, kDequant, kGemv, kGemvLoraDown, kTcGemm, kGemmFwd, kGemmBwd, kDropout,
-  kEpilogueBwd, kNorm, kVocabGemm, kVocabRows, kKinds
+  kEpilogueBwd, kNorm, kVocabGemm, kVocabRows, kGemmJoin, kKinds
 };
 const char* const kNames[kKinds] = {
     "nf4_quantize_kernel", "nf4_dequantize_kernel", "nf4_gemv_kernel",
     "gemv_lora_down_kernel", "tc_gemm_kernel",
     "nf4_gemm_kernel<fwd>", "nf4_gemm_kernel<bwd>", "dropout_apply_kernel",
-    "epilogue_bwd_kernel", "norm_residual_kernels", "vocab_gemm_kernel", "vocab_row_kernels"};
+    "epilogue_bwd_kernel", "norm_residual_kernels", "vocab_gemm_kernel", "vocab_row_kernels",
+    "nf4_gemm_join_kernel"};
 static_assert(kKinds == QLORA_KERNEL_KINDS, "kernel kinds");
 
 struct State {
@@ -344,6 +322,34 @@ struct Scope {
   }
 };
 }  // namespace prof
+
+// A kernel that calls pdl_wait() before it reads or writes memory, launched so that its start overlaps the
+// end of the kernel before it on the stream (which lets it by pdl_launch_dependents). prof_kind: the kind
+// it is timed as.
+template <typename... Params, typename... Args>
+int launch_after(int prof_kind, void (*kernel)(Params...), dim3 grid, unsigned threads, cudaStream_t st, size_t smem,
+                 const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t e;
+  {
+    prof::Scope ps(prof_kind, st);
+    e = cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...);
+  }
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return QLORA_ERR_CUDA;
+  }
+  return launch_status();
+}
 
 // ------------------------------------------------------------------------------------------
 // TMA tensor maps
@@ -864,8 +870,8 @@ int fwd_core(const uint16_t* X, const uint16_t* Xl, int64_t t, const nf4_weight*
     ga.kb_per_split = (ga.num_kb + shares - 1) / shares;
     if ((rc = launch_nf4_gemm<false, kEpiPartial>(mA, mP, mA2, mB2, ga, t, o, st, prof::kGemmFwd, shares, part)))
       return rc;
-    return launch_after(nf4_gemm_join_kernel, dim3(static_cast<unsigned>((t * (o / 8) + 255) / 256)), 256, st, 0, part,
-                        shares, Y, t, ga.N, ga.epi);
+    return launch_after(prof::kGemmJoin, nf4_gemm_join_kernel, dim3(static_cast<unsigned>((t * (o / 8) + 255) / 256)), 256,
+                        st, 0, part, shares, Y, t, ga.N, ga.epi);
   }
   return launch_nf4_gemm<false>(mA, mP, mA2, mB2, ga, t, o, st, prof::kGemmFwd);
 }
