@@ -19,8 +19,10 @@ constexpr unsigned kDevTimeout = 2u;
 constexpr unsigned kDevLaunch = 4u;
 constexpr unsigned kDevTarget = 8u;
 
-// A bounded wait gives up after this long (nanoseconds of the global timer). Every legitimate
-// wait inside one CTA is shorter than a millisecond at the sizes this library accepts.
+// A bounded wait gives up after this long (nanoseconds of the global timer). The longest legitimate wait
+// is that of the fused GEMM's epilogue for its accumulator: a whole K loop, 0.6 us per 64 inputs, 0.1 ms
+// at 11008 inputs and 0.2 s at 2^24 (some 2^27 inputs would pass the limit, and be reported). The
+// vocabulary loss waits for 8192 words or 512 inputs at a time, whatever its sizes.
 constexpr uint64_t kWaitTimeoutNs = 2000000000ull;
 
 __device__ __forceinline__ void report(unsigned bits) { atomicOr(&g_status, bits); }
@@ -127,18 +129,10 @@ __device__ __forceinline__ void cluster_sync() {
                ::: "memory");
 }
 
-// Arrive (release, cluster scope) on the mbarrier at the same shared-memory offset in CTA
-// `rank` of this cluster.
-__device__ __forceinline__ void mbar_arrive_remote(uint64_t* bar, uint32_t rank) {
-  uint32_t raddr;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(raddr) : "r"(smem_addr(bar)), "r"(rank));
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(raddr) : "memory");
-}
-
-// The same arrive with release at CTA scope, for an arrive that orders only what its thread did in
-// its own shared memory or tensor memory (whose one copy every reader uses): the cluster-scope
-// release above also waits for the thread's global writes, some 1400 cycles, which is longer than
-// a K-step's MMAs.
+// Arrive on the mbarrier at the same shared-memory offset in CTA `rank` of this cluster, with release at
+// CTA scope: it orders only what its thread did in its own shared memory or tensor memory (whose one copy
+// every reader uses). A release at cluster scope also waits for the thread's global writes, some 1400
+// cycles, which is longer than a K-step's MMAs.
 __device__ __forceinline__ void mbar_arrive_pair(uint64_t* bar, uint32_t rank) {
   uint32_t raddr;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(raddr) : "r"(smem_addr(bar)), "r"(rank));
@@ -163,36 +157,6 @@ __device__ __forceinline__ float4 ld_dsmem_f32x4(const float* local, uint32_t ra
                : "r"(raddr)
                : "memory");
   return v;
-}
-
-// try_wait with acquire at cluster scope (the phase was completed by another CTA's arrive).
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
-  uint32_t done;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(done)
-      : "r"(smem_addr(bar)), "r"(parity)
-      : "memory");
-  return done != 0;
-}
-
-__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity,
-                                                  volatile uint32_t* abort_flag) {
-  if (mbar_try_wait_cluster(bar, parity)) return true;
-  const uint64_t t0 = global_timer_ns();
-  for (uint32_t i = 1;; ++i) {
-    if (mbar_try_wait_cluster(bar, parity)) return true;
-    if ((i & 15u) == 0u) {
-      if (*abort_flag) return false;
-      if (global_timer_ns() - t0 > kWaitTimeoutNs) {
-        *abort_flag = 1u;
-        report(kDevTimeout);
-        return false;
-      }
-    }
-  }
 }
 
 // ------------------------------------------------------------------------------------------
@@ -401,24 +365,15 @@ __device__ __forceinline__ void fence_proxy_async_smem() {
 //   K-major:  rows of 64 bf16 along K; SBO = byte stride between 8-row groups; LBO unused.
 //   MN-major: rows of 64 bf16 along M/N; LBO = byte stride between 64-element M/N atoms,
 //             SBO = byte stride between groups of 8 K-rows.
-__device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
-  d |= static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16;
-  d |= static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32;
-  d |= static_cast<uint64_t>(1u) << 46;  // descriptor version for sm_100
-  d |= static_cast<uint64_t>(2u) << 61;  // SWIZZLE_128B
-  return d;
-}
-
-// The same descriptor in two halves, for loops over a ring of stages: the high half is a constant, and
-// the low half of another stage or K offset is this one plus (bytes >> 4) (shared memory addresses
-// stay below 2^18, so the address field never carries). Building each descriptor anew cost the one
-// thread that issues the MMAs some 880 cycles of dependent arithmetic per K-step of 8 MMAs.
+// In two halves, for loops over a ring of stages: the high half is a constant (SBO 1024, version 1 for
+// sm_100, SWIZZLE_128B), and the low half of another stage or K offset is this one plus (bytes >> 4)
+// (shared memory addresses stay below 2^18, so the address field never carries). Building each
+// descriptor anew cost the one thread that issues the MMAs some 880 cycles of dependent arithmetic per
+// K-step of 8 MMAs.
 __device__ __forceinline__ uint32_t sw128_desc_lo(uint32_t saddr, uint32_t lbo) {
   return ((saddr & 0x3FFFFu) >> 4) | (((lbo >> 4) & 0x3FFFu) << 16);
 }
-constexpr uint32_t kSw128DescHi = (1024u >> 4) | (1u << 14) | (2u << 29);   // SBO 1024
+constexpr uint32_t kSw128DescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
 __device__ __forceinline__ uint64_t sw128_desc_of(uint32_t lo) {
   uint64_t d;
   asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(lo), "r"(kSw128DescHi));

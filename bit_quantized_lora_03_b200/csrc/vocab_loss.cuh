@@ -68,7 +68,6 @@ constexpr int kTmemCols = 512;
 constexpr size_t smem_bytes() { return 1024 + STAGES * STAGE_BYTES + kStaging + 256; }
 static_assert(smem_bytes() <= 232448, "fits the opt-in shared memory of one CTA");
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
 }  // namespace vg
 
 enum VocabMode : int { kVocabStats = 0, kVocabScaled = 1, kVocabProb = 2, kVocabGrad = 3 };
