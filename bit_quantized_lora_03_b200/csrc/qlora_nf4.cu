@@ -491,15 +491,19 @@ EpiloguePlan plan_epilogue(int64_t t, int64_t h, int64_t o) {
 }
 
 // Whether the linear with the fused epilogue takes the tcgen05 path: above the GEMV's tokens, and from 9
-// tokens (the GEMV's second token tile) for a large weight where it is the shorter one by the estimates, in
-// us: the GEMM's and what its rank-r product adds, against the GEMV's (a fit over the shapes below and some
-// more). GEMV and GEMM measured at 16 tokens, rank 64: 8192 -> 8192 55, 40; 11008 -> 4096 45, 31; 22016 -> 8192
-// 100, 79; 4096 -> 16384 53, 42; 1024 -> 11008 37, 24; 8192 -> 10240 61, 56; 8192 -> 22016 96, 99; 8192 -> 28672
-// 113, 127; rank 16: 2048 -> 16384 32, 28; 8192 -> 8192 43, 40; 4096 -> 11008 33, 40; 1024 -> 20480 33, 38.
+// tokens (the GEMV's second token tile) where it is the shorter one by the estimates, in us: the GEMM's and
+// what its rank-r product adds, against the GEMV's (a fit over the shapes below and some more). GEMV and GEMM
+// measured at 16 tokens, the weight from HBM; rank 16: 512 -> 512 16.3, 11.7; 1024 -> 4096 16.6, 11.4;
+// 4096 -> 1024 16.6, 13.0; 8192 -> 512 17.0, 14.4; 1024 -> 8128 19.6, 16.2; 4096 -> 4096 21.3, 16.7; 2048 ->
+// 16384 27.9, 23.2; 1024 -> 20480 29.3, 30.4; 4096 -> 11008 30.8, 34.6; 8192 -> 8192 37.8, 35.5; 8192 -> 28672
+// 92.7, 120.6. Rank 64: 512 -> 512 25.4, 11.7; 4096 -> 1024 22.5, 13.5; 11008 -> 4096 41.8, 27.2; 8192 -> 8192
+// 47.4, 35.5; 8192 -> 10240 53.9, 49.8 (the one shape here that the estimates give to the slower path);
+// 8192 -> 22016 91.2, 96.4. Weights below 2^18 values keep the plain linear's kernels, and so its rank-r
+// product bit for bit, at some cost (256 -> 512, rank 16: 17.1, 10.2).
 bool epilogue_uses_gemm(int64_t t, int64_t h, int64_t o, int64_t r) {
   if (t > kGemvMaxTokens) return true;
   const double weights = static_cast<double>(h) * static_cast<double>(o);
-  if (t <= 8 || weights < (1 << 23)) return false;
+  if (t <= 8 || weights < (1 << 18)) return false;
   const EpiloguePlan p = plan_epilogue(t, h, o);
   return p.us + (p.shares > 1 ? 1.0 : 6.0) <
          15.0 + 0.1 * static_cast<double>(r) + 0.25e-3 * static_cast<double>(o) + 0.37e-6 * weights;
