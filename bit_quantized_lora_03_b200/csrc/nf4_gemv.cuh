@@ -395,11 +395,6 @@ __global__ void __launch_bounds__(gv::kThreads, 1)
   uint4 xc[NT][4], xn[NT][4];
   if (NT == 1 && kXAhead && nrun > 0) gemv_load_x<NT>(xc, args, cur.u0, g, q, 2 * cur.u0 + (q >> 1) < nblk);
 
-  // what finishing this run's first row tile will read, brought into L2 meanwhile
-  if (nrun > 0)
-    for (int c = lane; c < args.r; c += 32)
-      asm volatile("prefetch.global.L2 [%0];" ::"l"(args.L2 + static_cast<int64_t>(c) * args.o + cur.tile * kTileRows));
-
   if (threadIdx.x == 0) abort_flag = 0u;
   if (kWarps == 16) {
     // entry 16 j + warp, this lane's copy: one dynamic index into the levels, not two per entry
@@ -597,9 +592,20 @@ __global__ void __cluster_dims__(gd::kClusterCtas, 1, 1) __launch_bounds__(gd::k
   float acc[16][2];
 #pragma unroll
   for (int n = 0; n < 16; ++n) acc[n][0] = acc[n][1] = 0.f;
+  uint32_t la[4], lb[4];
+  auto load_l1 = [&](int64_t pb) {   // four of this thread's pairs of rows of L1
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int64_t pr = pb + u * nkg;
+      const int64_t k = 2 * (pr < p1 ? pr : p0);
+      la[u] = __ldg(reinterpret_cast<const uint32_t*>(L1 + k * r) + cp);
+      lb[u] = __ldg(reinterpret_cast<const uint32_t*>(L1 + (k + 1) * r) + cp);
+    }
+  };
   for (int64_t pp = p0; pp < p1; pp += piece) {
     const int64_t pe = pp + piece < p1 ? pp + piece : p1;
     const int np = static_cast<int>(pe - pp);
+    if (works) load_l1(pp + kg);    // (in flight while the activations are staged: one latency, not two)
     if (pp > p0) __syncthreads();   // the piece before has been read
     for (int n = tid >> 5; n < t; n += gd::kThreads / 32) {
       const uint32_t* xr = reinterpret_cast<const uint32_t*>(X + static_cast<int64_t>(n) * h) + pp;
@@ -607,14 +613,7 @@ __global__ void __cluster_dims__(gd::kClusterCtas, 1, 1) __launch_bounds__(gd::k
     }
     __syncthreads();
     for (int64_t pb = pp + kg; works && pb < pe; pb += 4 * nkg) {
-      uint32_t la[4], lb[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int64_t pr = pb + u * nkg;
-        const int64_t k = 2 * (pr < p1 ? pr : p0);
-        la[u] = __ldg(reinterpret_cast<const uint32_t*>(L1 + k * r) + cp);
-        lb[u] = __ldg(reinterpret_cast<const uint32_t*>(L1 + (k + 1) * r) + cp);
-      }
+      if (pb > pp + kg) load_l1(pb);
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const int64_t pr = pb + u * nkg;
