@@ -292,13 +292,16 @@ int vocab_core(const VocabCall& c, void* workspace, cudaStream_t st) {
     if ((rc = launch_narrow(vocab_narrow_grad_kernel, d, gctas, false, st, mWmn, mG))) return rc;
     VocabGemmArgs f{};
     f.N = d.h;
+    f.v = d.v;
     f.targets = c.targets;
+    f.ignore = c.ignore;
+    f.dloss = c.dloss;
+    f.dlse = c.dlse;
     f.W = c.W;
     f.target_factor = target_factor;
     if (stats) {
       f.redo = redo;
       f.factor = factor;
-      f.dloss = c.dloss;
     }
     return launch_after(prof::kVocabRows, vocab_narrow_join_kernel,
                         dim3(static_cast<unsigned>(d.tiles), static_cast<unsigned>((c.t + 1) / 2)), 256, st, 0, part, c.dX,
@@ -343,13 +346,16 @@ int vocab_core(const VocabCall& c, void* workspace, cudaStream_t st) {
     // g from lse: the backward alone, or again for a run whose scaled exponentials do not serve
     if ((rc = launch_vocab_gemm<kVocabProb>(mX, mWk, mGs, mX, a, pairs, !stats, st))) return rc;
     VocabGemmArgs d = plan_vocab_gemm(n, c.h, c.v, true, pairs);
+    d.v = a.N;
     d.targets = a.targets;
+    d.ignore = a.ignore;
+    d.dloss = a.dloss;
+    d.dlse = a.dlse;
     d.W = c.W;
     d.target_factor = target_factor;
     if (stats) {
       d.redo = redo;
       d.factor = factor;
-      d.dloss = a.dloss;
     }
     if ((rc = launch_vocab_gemm<kVocabGrad>(mG, mWmn, mD, mPart, d, pairs, false, st))) return rc;
     if (d.splits > 1) {

@@ -93,6 +93,7 @@ struct VocabGemmArgs {
                          // without which there is nothing to do. kVocabGrad: see row_factor
   const float* factor;   // kVocabGrad: NULL, or the rows' factors, by which (and by dloss) g is still to be multiplied
   float* target_factor;  // kVocabProb writes, kVocabGrad reads: the factors of the targets' W
+  int v;                 // kVocabGrad: the vocabulary (N is h there)
   const uint16_t* W;
 };
 
@@ -121,7 +122,8 @@ __device__ __forceinline__ VocabItem vocab_item(const VocabGemmArgs& a, int item
 }
 
 // dX from the second product: a row's factor and dloss times it, plus its target's factor times W[target].
-// Both are 1 without factors, or after kVocabProb ran again (g is then complete).
+// Without factors, or after kVocabProb ran again (g is then complete), both are 1, or 0 for a row that counts
+// for nothing: its g is zero, but zero times a word that is not finite is not.
 struct RowFactor {
   float f, d, ft;
   __device__ __forceinline__ float times(float v, float t) const {   // a row that counts for nothing: exactly zero
@@ -141,9 +143,15 @@ __device__ __forceinline__ RowFactor row_factor(const VocabGemmArgs& a, int row)
   r.f = r.d = r.ft = 0.f;
   r.w = nullptr;
   if (row >= 0) {
-    const bool whole = !a.factor || *a.redo != 0u;
-    r.f = whole ? 1.f : a.factor[row];
-    r.d = whole ? 1.f : a.dloss[row];
+    if (a.factor && *a.redo == 0u) {
+      r.f = a.factor[row];   // (zero for a row that is not counted)
+      r.d = a.dloss[row];
+    } else {
+      const int64_t y = a.targets[row];
+      const bool counted = y >= 0 && y < a.v && y != a.ignore;
+      r.f = (counted && a.dloss[row] != 0.f) || (a.dlse && a.dlse[row] != 0.f) ? 1.f : 0.f;
+      r.d = 1.f;
+    }
     r.ft = a.target_factor[row];
     if (r.ft != 0.f) r.w = a.W + a.targets[row] * a.N;   // (counted: inside the vocabulary)
   }
@@ -353,6 +361,8 @@ __global__ void __launch_bounds__(vg::kThreads, 1)
       const int row0 = it.m0 + rank * 128 + quad * 32, row = row0 + lane;
       const int n0 = it.n0 + half * PIECE;   // this warp's first column
       const bool rok = row < args.M;
+      RowFactor rf;
+      if (kMode == kVocabGrad) rf = row_factor(args, it.part < 0 && rok ? row : -1);   // (loaded under the products)
       // the tile's sums over its accumulations
       float s[PIECE];
 #pragma unroll
@@ -372,7 +382,6 @@ __global__ void __launch_bounds__(vg::kThreads, 1)
       }
       if (!ok) break;
       if (kMode == kVocabGrad) {
-        const RowFactor rf = row_factor(args, it.part < 0 && rok ? row : -1);
 #pragma unroll
         for (int c = 0; c < PIECE; c += 64) {
           uint4 q[8];
@@ -1010,6 +1019,7 @@ __global__ void __launch_bounds__(256)
   const VocabItem it = vocab_item(b, a.whole + tile);
   const int row = it.m0 + r, col = it.n0 + lane * 8;
   if (row >= a.M || col >= a.N) return;   // N % 8 == 0
+  const RowFactor rf = row_factor(a, row);
   float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   for (int p = 0; p < a.splits; ++p) {
     const float4* q = reinterpret_cast<const float4*>(
@@ -1018,7 +1028,7 @@ __global__ void __launch_bounds__(256)
     s[0] += u.x; s[1] += u.y; s[2] += u.z; s[3] += u.w;
     s[4] += w.x; s[5] += w.y; s[6] += w.z; s[7] += w.w;
   }
-  row_factor(a, row).apply(s, col);
+  rf.apply(s, col);
   *reinterpret_cast<uint4*>(dX + static_cast<int64_t>(row) * a.N + col) = pack8(s);
 }
 

@@ -5,7 +5,7 @@ import torch
 
 from bit_quantized_lora_03_b200 import binding as B
 
-from block_util import U16, U32, assert_within
+from block_util import U16, U32, assert_within, randn
 from gpu_util import require_gpu
 
 pytestmark = pytest.mark.gpu
@@ -82,3 +82,35 @@ def test_gradient_over_a_long_vocabulary_is_summed_in_pieces(t, h, v):
     for got, name in ((dX, "dX"), (back, "dX from lse")):
         assert_within(got, want, U16 * (want.abs() + e) + e, name)
     assert B.last_status() == 0
+
+
+@pytest.mark.parametrize("word", [float("-inf"), float("nan")])
+@pytest.mark.parametrize("t", [30, 300])
+def test_rows_that_count_for_nothing_get_zero_whatever_the_words_hold(t, word):
+    """Also in the gradient from lse, and in the one-call form where a loss above 60 has the run computed again."""
+    h, v = 64, 700
+    X, W = torch.ones(t, h), torch.zeros(v, h)
+    W[7] = word
+    y = torch.arange(t) % 500 + 20
+    off = torch.arange(t) % 3 == 0
+    y[off] = -100
+    X, W, y, off = X.bfloat16().cuda(), W.bfloat16().cuda(), y.cuda(), off.cuda()
+    d = torch.ones(t, device="cuda")
+    W[9] = 2.0      # a word of logit 128: every loss is
+    _, lse, dX = B.qlora_vocab_loss_fwd_bwd(X, W, y, d)
+    assert not dX[off].any()
+    assert not B.qlora_vocab_loss_bwd(X, W, y, lse, d)[off].any()
+    e = torch.where(torch.arange(t, device="cuda") % 6 == 0, 0.0, 1.0)
+    back = B.qlora_vocab_loss_bwd(X, W, y, lse, d, dlse=e)
+    assert not back[::6].any()      # neither counted nor with a gradient of lse
+    assert torch.isnan(back[3::6]).all()    # the formula's zero times -inf, or NaN
+
+
+@pytest.mark.parametrize("t", [30, 300])
+def test_gradients_of_loss_and_lse_that_cancel(t):
+    """dlse = -dloss leaves a = 0 and b = dloss: dX is -b W[y], exactly."""
+    h, v = 72, 700
+    X, W, y = randn((t, h), 1.0, 1).cuda(), randn((v, h), 0.5, 2).cuda(), (torch.arange(t) % v).cuda()
+    d = torch.full((t,), 0.25, device="cuda")
+    _, lse = B.qlora_vocab_loss_fwd(X, W, y)
+    assert torch.equal(B.qlora_vocab_loss_bwd(X, W, y, lse, d, dlse=-d), -0.25 * W[y])
