@@ -363,20 +363,26 @@ __global__ void __launch_bounds__(vg::kThreads, 1)
       const bool rok = row < args.M;
       RowFactor rf;
       if (kMode == kVocabGrad) rf = row_factor(args, it.part < 0 && rok ? row : -1);   // (loaded under the products)
-      // the tile's sums over its accumulations
+      // the tile's sums over its accumulations: the first one as it comes, all of its columns in flight, the
+      // others 16 columns at a time (the sums leave no room for more)
       float s[PIECE];
-#pragma unroll
-      for (int e = 0; e < PIECE; ++e) s[e] = 0.f;
 #pragma unroll 1
       for (int kc = it.kb0; kc < it.kb1; kc = chunk_end(it, kc)) {
         if (!wait_acc()) { ok = false; break; }
+        const uint32_t acc = lane_addr + (n & 1) * BN;
+        if (kc == it.kb0) {
 #pragma unroll
-        for (int c = 0; c < PIECE; c += 16) {   // (16 at a time: the sums leave no room for more)
-          uint32_t v[16];
-          tmem_ld_16(lane_addr + (n & 1) * BN + c, v);
+          for (int c = 0; c < PIECE; c += 16) tmem_ld_16(acc + c, *reinterpret_cast<uint32_t(*)[16]>(&s[c]));
           tmem_ld_wait();
+        } else {
 #pragma unroll
-          for (int e = 0; e < 16; ++e) s[c + e] += __uint_as_float(v[e]);
+          for (int c = 0; c < PIECE; c += 16) {
+            uint32_t v[16];
+            tmem_ld_16(acc + c, v);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) s[c + e] += __uint_as_float(v[e]);
+          }
         }
         release_acc();
       }
