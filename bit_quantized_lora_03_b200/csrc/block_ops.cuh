@@ -78,7 +78,7 @@ constexpr int kVocabMaxParts = kMaxSms;   // partial tiles of a split K
 
 // Up to this many tokens go through the kernels that stream W past them (one 256-token tile of the
 // others is computed whole whatever it holds). Measured on 32000 x 4096, loss and
-// gradient: 101 us at 16 tokens, 113 at 64, 120 at 80, against 129 at 96 and 133 at 200.
+// gradient: 102 us at 16 tokens, 121 at 64, 130 at 80, against 134 at 81, 143 at 96 and 152 at 200.
 constexpr int64_t kVocabNarrowTokens = vn::kMaxTokens;
 constexpr int64_t kFewRows = 1024;   // rows that get a CTA each in the kernels over rows (a warp each above)
 

@@ -12,7 +12,8 @@
 // Phi(z) = 1 - q/2 (z >= 0) or q/2, q = erfc(|z|/sqrt 2) by Abramowitz and Stegun 7.1.26, a polynomial
 // of fifth degree in 1/(1 + 0.3275911 |z|/sqrt 2) times exp(-z^2/2), off by at most 1.5e-7: one
 // exponential and one division, and the same exponential serves gelu's derivative (erff took 1.8
-// times the time of silu in the GEMM's epilogue, this 1.1).
+// times the time of silu in the GEMM's epilogue, this 1.1). Relative to gelu's own negative tail that is
+// 5e-5 at -3, 1.6e-3 at -5 and 3.6e-3 at -6, half a step of bf16; gelu is below 6e-9 behind that.
 #pragma once
 
 #include "norm_residual.cuh"

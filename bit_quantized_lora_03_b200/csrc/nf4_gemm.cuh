@@ -22,7 +22,7 @@
 //    shares of a split K that nf4_gemm_join_kernel finishes.
 //    Bound: the tensor cores. Copies and dequantized tiles of both CTAs are counted on the even
 //    CTA's barriers, so its issuing warp waits for no relay. Measured, 4096 tokens, 4096 -> 11008:
-//    259 us plain (1.45 PFLOP/s), 288 with bias, SiLU and Z kept.
+//    257 us plain (1.46 PFLOP/s), 287 with bias, SiLU and Z kept.
 //
 // (tc_gemm.cuh holds the plain tcgen05 GEMM for the rank-r products.)
 //

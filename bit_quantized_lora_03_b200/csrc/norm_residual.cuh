@@ -22,8 +22,8 @@
 // adds the partials in a fixed order (no atomics: results repeat bit for bit).
 //
 // Bound: HBM, 2 bytes for each value of x, y, x', n (forward: 4 per element of a row's h) and of dx', dn,
-// x', y, dx, dy (backward: 6). Measured: forward, 2048 x 8192, 24.5 us (5.5 TB/s); backward, 4096 x 4096,
-// 39.7 us (5.1 TB/s) and 4.8 us for the partial rows; one row 2.7 us, the latency of two reductions.
+// x', y, dx, dy (backward: 6). Measured: forward, 2048 x 8192, 24.3 us (5.5 TB/s); backward, 4096 x 4096,
+// 39.9 us (5.0 TB/s) and 4.8 us for the partial rows; one row 2.5 us, the latency of two reductions.
 #pragma once
 
 #include "qlora_common.cuh"

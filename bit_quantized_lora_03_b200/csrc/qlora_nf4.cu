@@ -469,8 +469,9 @@ constexpr int64_t kGemvMaxTokens = 16;
 // Shares of K of the linear with the fused epilogue on the tcgen05 path: its tiles of 512 tokens x 256
 // outputs leave most of the card idle for a few hundred tokens. A K-step takes about 0.6 us (0.43 with
 // one accumulator) and a share 11 us (7) besides, a round of pairs as long as one share; the shares cost
-// their fp32 traffic at some 5 TB/s and another launch. 4096 -> 4096: 17 tokens 64 -> 18 us with the join;
-// 11008 -> 4096: 777 tokens 150 -> 83 us. Planned for 148 SMs, so that the workspace is a host function.
+// their fp32 traffic at some 5 TB/s and another launch. Whole calls from a graph, K whole and split: 4096 ->
+// 4096, 17 tokens 34 -> 17 us; 11008 -> 4096, 777 tokens 108 -> 75. Planned for 148 SMs, so that the workspace
+// is a host function.
 struct EpiloguePlan {
   int shares;
   double us;   // of the GEMM and the join

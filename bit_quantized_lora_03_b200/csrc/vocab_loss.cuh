@@ -39,8 +39,8 @@
 // half of A and half of B), a TMA ring of three stages of two K-steps, and two accumulators in tensor
 // memory, so that a tile's epilogue (eight warps) runs under the next tile's products. g is rounded to
 // bf16 because it is an operand of a bf16 product: 2^-8 of each term at most, as dX's own rounding.
-// Measured on 32000 x 4096, 4096 tokens: loss and gradient 1610 us, two products at 1.33 PFLOP/s, where
-// the card is at its power limit (1.39 in a plain bf16 product); 1 token: loss 54 us, W read once.
+// Measured on 32000 x 4096, 4096 tokens: loss and gradient 1590 to 1690 us, two products at 1.27 to 1.35
+// PFLOP/s, where the card is at its power limit (1.39 in a plain bf16 product); 1 token: loss 50 us, W read once.
 //
 // Every wait is bounded (qlora::mbar_wait); on expiry the CTA reports QLORA_DEV_TIMEOUT, stops
 // issuing, waits for its own copies and MMAs in flight, frees TMEM and returns.
