@@ -91,3 +91,31 @@ def test_inputs_freed_at_once_are_not_given_out_again(name):
     for shape, dtype, ptr in kinds:
         assert not any(a <= ptr < b for a, b in got), (name, tuple(shape), dtype)
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("name", ["linear_fwd_epilogue", "epilogue_bwd", "norm_residual_bwd", "vocab_loss_fwd_bwd", "vocab_loss_bwd"])
+def test_calls_on_a_second_stream_inside_a_capture(name):
+    """The call joins the capture through its own stream; some of its inputs are made, and freed, in it."""
+    make, call = CALLS[name]
+    values, side = make(), torch.cuda.Stream()
+    want = call(None, *values)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        copies = [v.clone() if torch.is_tensor(v) else v for v in values]
+        side.wait_stream(torch.cuda.current_stream())
+        out = call(side, *copies)
+        torch.cuda.current_stream().wait_stream(side)
+        del copies
+        after = torch.zeros(1 << 20, device="cuda")     # noqa: F841
+    for _ in range(2):
+        for t in _tensors([o for o in (out if isinstance(out, tuple) else (out,)) if o is not None]):
+            t.zero_()
+        g.replay()
+    torch.cuda.synchronize()
+    pairs = zip(out, want) if isinstance(out, tuple) else ((out, want),)
+    for a, b in pairs:
+        assert a is None and b is None or torch.equal(a, b)
+    del g, out, values
+    torch.cuda.synchronize()
+    assert B.last_status() == 0
